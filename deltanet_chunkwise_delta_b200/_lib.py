@@ -10,23 +10,27 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
 from . import build as _build
 
 DN_OK, DN_ERR_INVALID_ARG, DN_ERR_UNSUPPORTED, DN_ERR_ALIAS, DN_ERR_CUDA, \
-    DN_ERR_WORKSPACE, DN_ERR_SEQLENS, DN_ERR_TIMEOUT = range(8)
+    DN_ERR_WORKSPACE, DN_ERR_SEQLENS, DN_ERR_TIMEOUT, DN_ERR_SLOTS = range(9)
 DN_F32, DN_BF16, DN_I32 = 0, 1, 2
+DN_ACT_SILU, DN_ACT_SIGMOID = 0, 1
 
 EXPORTED = ("deltanet_fwd", "deltanet_fwd_ex", "gated_deltanet_fwd", "gated_deltanet_fwd_ex",
             "gated_deltaproduct_fwd", "gated_deltaproduct_fwd_ex", "deltanet_fwd_states",
             "deltanet_status_string",
             "deltanet_get_error", "deltanet_release_workspace", "deltanet_last_schedule",
             "deltanet_fwd_noalloc", "deltanet_last_launches", "deltanet_set_kernel_events",
-            "deltanet_test_set_wait", "kda_fwd", "kda_fwd_ex")
+            "deltanet_test_set_wait", "kda_fwd", "kda_fwd_ex",
+            "deltanet_step", "deltanet_scan_fwd", "deltanet_scan_bwd", "deltanet_scan_step",
+            "deltanet_norm_fwd", "deltanet_norm_bwd", "deltanet_norm_workspace")
 
 
 class DnTensor(ctypes.Structure):
@@ -104,6 +108,19 @@ def load(path: Optional[str] = None):
         lib.deltanet_last_schedule.restype = None
         lib.deltanet_last_schedule.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
                                                ctypes.POINTER(ctypes.c_int)]
+        # these take the descriptors' addresses as integers (see _descriptors)
+        V, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+        lib.deltanet_step.argtypes = [V, V, V, V, V, I, V, V, V, V]
+        lib.deltanet_scan_fwd.argtypes = [V] * 7
+        lib.deltanet_scan_bwd.argtypes = [V] * 10
+        lib.deltanet_scan_step.argtypes = [V] * 6
+        lib.deltanet_norm_fwd.argtypes = [V, V, V, I, V, V, V, F, V, V, V]
+        lib.deltanet_norm_bwd.argtypes = [V, V, V, I, V, V, V, F] + [V] * 10
+        for f in (lib.deltanet_step, lib.deltanet_scan_fwd, lib.deltanet_scan_bwd,
+                  lib.deltanet_scan_step, lib.deltanet_norm_fwd, lib.deltanet_norm_bwd):
+            f.restype = ctypes.c_int
+        lib.deltanet_norm_workspace.restype = ctypes.c_int64
+        lib.deltanet_norm_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64]
         _lib = lib
         return lib
 
@@ -355,6 +372,236 @@ def deltanet_fwd_noalloc(q, k, v, beta, initial_state=None, chunk_size: int = 64
     if st != DN_OK:
         raise DeltaNetError(st, status_string(st))
     return out, final_state
+
+
+# dn_tensor as bytes: the operators below are called once per token and layer when decoding,
+# where filling ctypes structures field by field would take longer than the kernel.
+_DESC = struct.Struct("@Pii8q")
+assert _DESC.size == ctypes.sizeof(DnTensor)
+_PAD = (0, 0, 0, 0)
+
+
+def _descriptors(*tensors):
+    """Descriptors of the given tensors (None stays None) in one buffer: (buffer, addresses).
+    The buffer has to outlive the call that gets the addresses."""
+    buf = ctypes.create_string_buffer(_DESC.size * len(tensors))
+    base = ctypes.addressof(buf)
+    addr, at = [], 0
+    for t in tensors:
+        if t is None:
+            addr.append(None)
+            continue
+        dt, n = _DT.get(t.dtype), t.dim()
+        if dt is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        if not 1 <= n <= 4:
+            raise ValueError("1 to 4 dimensions")
+        pad = _PAD[n:]
+        _DESC.pack_into(buf, at, t.data_ptr(), dt, n, *t.shape, *pad, *t.stride(), *pad)
+        addr.append(base + at)
+        at += _DESC.size
+    return buf, addr
+
+
+class _On:
+    """The device and stream of one call: entering makes them current for the allocations
+    and the launch where they are not, ``handle`` is the stream's handle."""
+
+    def __init__(self, name, stream, lead, *others):
+        if not isinstance(lead, torch.Tensor) or not lead.is_cuda:
+            raise ValueError(f"{name} runs on CUDA tensors only")
+        dev = lead.device
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(dev)
+        self.handle = _stream_handle(dev, stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _check(st: int) -> None:
+    if st != DN_OK:
+        raise DeltaNetError(st, status_string(st))
+
+
+def deltanet_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
+                  state: torch.Tensor, g: Optional[torch.Tensor] = None, n_h: int = 1,
+                  slot_idx: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  stream=None):
+    """The delta-rule recurrences for the few tokens of a decoding step, on a cache of
+    states updated in place.
+
+    q [N, T, H, d_k]; k [N, T * n_h, H, d_k], v [N, T * n_h, H, d_v] and beta [N, T * n_h, H]
+    with a token's n_h writes on consecutive rows; g None (DeltaNet), [N, T, H] (Gated
+    DeltaNet, Gated Delta Product) or [N, T, H, d_k] (Kimi Delta Attention), ln a in fp32;
+    state [M, H, d_k, d_v] fp32; slot_idx int32 [N] names each request's row of it (-1: a
+    padding request, whose rows of out are zero), None: request n uses row n.  Returns out
+    [N, T, H, d_v].  Asynchronous on ``stream`` (default: torch's current stream)."""
+    on = _On("deltanet_step", stream, q, k, v, beta, state, g, slot_idx, out)
+    with on as handle:
+        if out is None:
+            out = torch.empty((*q.shape[:3], v.shape[-1]), dtype=q.dtype, device=q.device)
+        keep, a = _descriptors(q, k, v, beta, g, state, slot_idx, out)
+        _check(load().deltanet_step(*a[:5], int(n_h), *a[5:], handle))
+    return out
+
+
+def deltanet_scan_fwd(x: torch.Tensor, g: torch.Tensor,
+                      initial_state: Optional[torch.Tensor] = None,
+                      cu_seqlens: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None,
+                      final_state: Optional[torch.Tensor] = None,
+                      output_final_state: bool = True, stream=None):
+    """The gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t, channel by channel.
+
+    x [B, T, D] bf16 or fp32; g [B, T, D] fp32 (or bf16 with bf16 x), ln of the decay;
+    initial_state [N, D] fp32 or None; cu_seqlens int32 [N+1] or None.  Returns (out,
+    final_state or None): every h_t in the dtype of x and the last one of each sequence
+    in fp32."""
+    on = _On("deltanet_scan_fwd", stream, x, g, initial_state, cu_seqlens, out, final_state)
+    with on as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if final_state is None and output_final_state:
+            n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+            final_state = torch.empty((n, x.shape[-1]), dtype=torch.float32, device=x.device)
+        keep, a = _descriptors(x, g, initial_state, cu_seqlens, out, final_state)
+        _check(load().deltanet_scan_fwd(*a, handle))
+    return out, final_state
+
+
+def deltanet_scan_bwd(g: torch.Tensor, out: torch.Tensor, d_out: torch.Tensor,
+                      initial_state: Optional[torch.Tensor] = None,
+                      cu_seqlens: Optional[torch.Tensor] = None,
+                      d_final_state: Optional[torch.Tensor] = None,
+                      d_x: Optional[torch.Tensor] = None, d_g: Optional[torch.Tensor] = None,
+                      d_initial_state: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of ``deltanet_scan_fwd`` from its output ``out``: (d_x, d_g,
+    d_initial_state), the last where initial_state (or a buffer for it) is given, else
+    None.  d_final_state [N, D] fp32, or None for zeros."""
+    on = _On("deltanet_scan_bwd", stream, g, out, d_out, initial_state, cu_seqlens, d_final_state,
+             d_x, d_g, d_initial_state)
+    with on as handle:
+        if d_x is None:
+            d_x = torch.empty(out.shape, dtype=out.dtype, device=g.device)
+        if d_g is None:
+            d_g = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+        if d_initial_state is None and initial_state is not None:
+            d_initial_state = torch.empty(initial_state.shape, dtype=torch.float32, device=g.device)
+        keep, a = _descriptors(g, out, initial_state, cu_seqlens, d_out, d_final_state, d_x, d_g,
+                               d_initial_state)
+        _check(load().deltanet_scan_bwd(*a, handle))
+    return d_x, d_g, d_initial_state
+
+
+def deltanet_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                       slot_idx: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None):
+    """The gated linear recurrence for the few tokens of a decoding step: x, g [N, T, D],
+    state [M, D] fp32 updated in place, slot_idx as ``deltanet_step``.  Returns out
+    [N, T, D]."""
+    on = _On("deltanet_scan_step", stream, x, g, state, slot_idx, out)
+    with on as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        keep, a = _descriptors(x, g, state, slot_idx, out)
+        _check(load().deltanet_scan_step(*a, handle))
+    return out
+
+
+_ACTIVATIONS = {"silu": DN_ACT_SILU, "sigmoid": DN_ACT_SIGMOID}
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation {name!r}: one of {sorted(_ACTIVATIONS)}")
+    return _ACTIVATIONS[name]
+
+
+def deltanet_norm_fwd(y: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None,
+                      next_weight: Optional[torch.Tensor] = None, activation: str = "silu",
+                      eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                      residual_out: Optional[torch.Tensor] = None, stream=None):
+    """The norms before and after a block with its gate and residual scale, over the last
+    dimension d: y1 = rms_norm(y, weight), y2 = y1 activation(gate), r' = residual + scale y2,
+    n = rms_norm(r', next_weight), each part where its operand is given.
+
+    y, gate [.., d] in one dtype (bf16 or fp32); residual in that dtype or fp32; weight,
+    scale, next_weight [d] fp32 or bf16; activation "silu" or "sigmoid".  Returns (out,
+    residual_out): without residual (y2, None); with it (n, r'), n None without
+    next_weight."""
+    act = _activation(activation)
+    on = _On("deltanet_norm_fwd", stream, y, weight, gate, residual, scale, next_weight, out,
+             residual_out)
+    with on as handle:
+        if out is None and (residual is None or next_weight is not None):
+            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        if residual_out is None and residual is not None:
+            residual_out = torch.empty(y.shape, dtype=residual.dtype, device=y.device)
+        keep, a = _descriptors(y, weight, gate, residual, scale, next_weight, out, residual_out)
+        _check(load().deltanet_norm_fwd(*a[:3], act, *a[3:6], float(eps), *a[6:], handle))
+    return out, residual_out
+
+
+class NormGrads(NamedTuple):
+    """Gradients of ``deltanet_norm_fwd``'s operands; None where one was not given.  Those of
+    weight, scale and next_weight are fp32."""
+    d_y: torch.Tensor
+    d_weight: Optional[torch.Tensor]
+    d_gate: Optional[torch.Tensor]
+    d_residual: Optional[torch.Tensor]
+    d_scale: Optional[torch.Tensor]
+    d_next_weight: Optional[torch.Tensor]
+
+
+def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
+                      weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None,
+                      next_weight: Optional[torch.Tensor] = None,
+                      d_residual_out: Optional[torch.Tensor] = None, activation: str = "silu",
+                      eps: float = 1e-6, stream=None, d_y: Optional[torch.Tensor] = None,
+                      d_gate: Optional[torch.Tensor] = None,
+                      d_residual: Optional[torch.Tensor] = None) -> NormGrads:
+    """Gradients of ``deltanet_norm_fwd`` from its inputs, the gradient d_out of out (None
+    where the forward call has no out) and d_residual_out of residual_out (None: zeros,
+    where next_weight is given).  Buffers for the row gradients may be passed in."""
+    act = _activation(activation)
+    on = _On("deltanet_norm_bwd", stream, y, d_out, weight, gate, residual, scale, next_weight,
+             d_residual_out, d_y, d_gate, d_residual)
+    with on as handle:
+        dev, lib = y.device, load()
+        like = lambda t, given: given if given is not None or t is None else             torch.empty(t.shape, dtype=t.dtype, device=dev)
+        d_y, d_gate, d_residual = like(y, d_y), like(gate, d_gate), like(residual, d_residual)
+        params = [t is not None for t in (weight, scale, next_weight)]
+        d, work, sums = y.shape[-1], None, [None] * 3
+        if any(params):
+            sums = [torch.empty(d, dtype=torch.float32, device=dev) if p else None for p in params]
+            n = int(lib.deltanet_norm_workspace(y.numel() // d if d else 0, d))
+            work = torch.empty(n, dtype=torch.float32, device=dev) if n else None
+        keep, a = _descriptors(y, weight, gate, residual, scale, next_weight, d_out,
+                               d_residual_out, d_y, sums[0], d_gate, d_residual, sums[1], sums[2],
+                               work)
+        _check(lib.deltanet_norm_bwd(*a[:3], act, *a[3:6], float(eps), *a[6:], handle))
+    return NormGrads(d_y, sums[0], d_gate, d_residual, sums[1], sums[2])
 
 
 def get_error(stream=None, device=None) -> int:

@@ -15,6 +15,7 @@
 #include "../../include/deltanet.h"
 #include "dn_chain.cuh"
 #include "dn_common.cuh"
+#include "dn_host.h"
 #include "dn_prep.cuh"
 #include "dn_sched.cuh"
 #include "dn_tc.cuh"
@@ -47,65 +48,6 @@ std::map<std::pair<int, cudaStream_t>, StreamWs> g_ws;
 std::set<std::pair<int, const void*>> g_attr_done;
 std::map<int, int> g_dev_ok;     // device -> 1 ok, 0 unsupported
 std::map<int, int> g_dev_sms;
-
-int64_t elem_size(int32_t dt) { return dt == DN_F32 ? 4 : dt == DN_BF16 ? 2 : dt == DN_I32 ? 4 : 0; }
-
-bool shape_eq(const dn_tensor* t, int ndim, const int64_t* dims) {
-    if (!t || t->ndim != ndim) return false;
-    for (int i = 0; i < ndim; ++i)
-        if (t->shape[i] != dims[i]) return false;
-    return true;
-}
-
-int64_t numel(const dn_tensor* t) {
-    int64_t n = 1;
-    for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-    return n;
-}
-
-// Byte span [lo, hi) touched by a strided view (non-negative strides only).
-bool span(const dn_tensor* t, uintptr_t& lo, uintptr_t& hi) {
-    lo = hi = 0;
-    if (!t || numel(t) == 0) return true;
-    int64_t last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-        if (t->stride[i] < 0) return false;
-        last += (t->shape[i] - 1) * t->stride[i];
-    }
-    const int64_t es = elem_size(t->dtype);
-    lo = reinterpret_cast<uintptr_t>(t->data);
-    hi = lo + static_cast<uintptr_t>((last + 1) * es);
-    return true;
-}
-
-bool overlap(const dn_tensor* a, const dn_tensor* b) {
-    uintptr_t a0, a1, b0, b1;
-    span(a, a0, a1);
-    span(b, b0, b1);
-    if (a0 == a1 || b0 == b1) return false;
-    return a0 < b1 && b0 < a1;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// q/k/v/out: [B, T, H, d], stride[3] == 1, 16-byte aligned rows and strides.
-bool token_tensor_ok(const dn_tensor* t) {
-    if (t->stride[3] != 1) return false;
-    const int64_t es = elem_size(t->dtype);
-    if (numel(t) == 0) return true;
-    if (!t->data || !aligned16(t->data)) return false;
-    for (int i = 0; i < 3; ++i)
-        if (t->stride[i] < 0 || (t->stride[i] * es) % 16 != 0) return false;
-    return true;
-}
-
-bool state_tensor_ok(const dn_tensor* t, int64_t dv) {
-    if (t->dtype != DN_F32 || t->stride[3] != 1 || t->stride[2] != dv) return false;
-    if (numel(t) == 0) return true;
-    if (!t->data || !aligned16(t->data)) return false;
-    return t->stride[0] >= 0 && t->stride[1] >= 0 && (t->stride[0] * 4) % 16 == 0 &&
-           (t->stride[1] * 4) % 16 == 0;
-}
 
 dn_status device_check(int& dev, int& sms) {
     if (cudaGetDevice(&dev) != cudaSuccess) return DN_ERR_CUDA;
@@ -752,6 +694,7 @@ const char* deltanet_status_string(dn_status s) {
         case DN_ERR_WORKSPACE: return "DN_ERR_WORKSPACE: workspace allocation failed or limit exceeded";
         case DN_ERR_SEQLENS: return "DN_ERR_SEQLENS: invalid cu_seqlens contents";
         case DN_ERR_TIMEOUT: return "DN_ERR_TIMEOUT: a bounded device wait gave up";
+        case DN_ERR_SLOTS: return "DN_ERR_SLOTS: a slot index out of range or given twice";
     }
     return "unknown dn_status";
 }
@@ -778,6 +721,7 @@ dn_status deltanet_get_error(void* stream_ptr) {
     }
     if (h == kErrSeqlens) return DN_ERR_SEQLENS;
     if (h == kErrTimeout) return DN_ERR_TIMEOUT;
+    if (h == DN_ERR_SLOTS) return DN_ERR_SLOTS;
     return DN_OK;
 }
 
@@ -792,6 +736,28 @@ void dn_wait_settings(unsigned long long* wait_ns, int* stall_chunk) {
     *wait_ns = g_wait_ns;
     *stall_chunk = g_stall_chunk;
 }
+
+dn_status dn_device_check(int& dev, int& sms) { return device_check(dev, sms); }
+
+dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag) {
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        auto it = g_ws.find(std::make_pair(dev, stream));
+        if (it != g_ws.end() && it->second.flag) {
+            *flag = it->second.flag;
+            return DN_OK;
+        }
+    }
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return DN_ERR_CUDA;
+    if (cap != cudaStreamCaptureStatusNone) return DN_ERR_WORKSPACE;
+    StreamWs ws;
+    const dn_status st = get_ws(dev, stream, 0, ws);
+    if (st == DN_OK) *flag = ws.flag;
+    return st;
+}
+
+void dn_note_launches(int n) { g_last_launches = n; }
 
 extern "C" {
 

@@ -1,0 +1,54 @@
+// Element access shared by the operators around the delta-rule kernels: bf16 and fp32
+// values in registers as fp32, alone or V at a time.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace dn {
+
+template <typename E>
+__device__ __forceinline__ float ld_elem(const E* p) {
+    if constexpr (sizeof(E) == 2) return __bfloat162float(*p);
+    else return *p;
+}
+template <typename E>
+__device__ __forceinline__ void st_elem(E* p, float x) {
+    if constexpr (sizeof(E) == 2) *p = __float2bfloat16_rn(x);
+    else *p = x;
+}
+
+// Four consecutive elements (8-byte aligned bf16, 16-byte aligned fp32).
+template <typename E>
+__device__ __forceinline__ float4 ld_elem4(const E* p) {
+    if constexpr (sizeof(E) == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+    } else {
+        return *reinterpret_cast<const float4*>(p);
+    }
+}
+template <typename E>
+__device__ __forceinline__ void st_elem4(E* p, float4 x) {
+    if constexpr (sizeof(E) == 2) {
+        __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    } else {
+        *reinterpret_cast<float4*>(p) = x;
+    }
+}
+
+// A [d] parameter vector in fp32 or bf16.
+struct ParamVec {
+    const void* p;  // null: not given
+    int bf16;
+};
+__device__ __forceinline__ float ld_param(const ParamVec& v, int j) {
+    return v.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v.p)[j])
+                  : static_cast<const float*>(v.p)[j];
+}
+
+}  // namespace dn

@@ -38,7 +38,8 @@ typedef enum {
     DN_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed */
     DN_ERR_WORKSPACE = 5,     /* workspace allocation failed */
     DN_ERR_SEQLENS = 6,       /* cu_seqlens content invalid (reported by deltanet_get_error) */
-    DN_ERR_TIMEOUT = 7        /* a bounded device-side wait gave up (reported by deltanet_get_error) */
+    DN_ERR_TIMEOUT = 7,       /* a bounded device-side wait gave up (reported by deltanet_get_error) */
+    DN_ERR_SLOTS = 8          /* slot_idx content invalid (reported by deltanet_get_error) */
 } dn_status;
 
 typedef enum { DN_F32 = 0, DN_BF16 = 1, DN_I32 = 2 } dn_dtype;
@@ -290,13 +291,187 @@ dn_status deltanet_fwd_noalloc(const dn_tensor* q, const dn_tensor* k, const dn_
                                int chunk_size, dn_tensor* out, dn_tensor* final_state,
                                void* stream);
 
+/*
+ * deltanet_step -- the delta-rule recurrences for the few tokens that a decoding
+ * step brings per request, on a cache of states that is updated in place.
+ *
+ * For every request n and head h, with S = state[slot_idx[n], h], token after
+ * token (the token forms of "Linear Attention, Visualized": DeltaNet, Gated
+ * DeltaNet, Gated Delta Product and Kimi Delta Attention):
+ *
+ *     S <- Diag(a_t) S                                 (a_t = exp g_t; 1 without g)
+ *     S <- S + k_j^T beta_j (v_j - k_j S)              for the token's n_h writes j
+ *     o_t = q_t S
+ *
+ *   q             [N, T, H, d_k]        bf16 or fp32 (the same dtype for q, k, v, out)
+ *   k             [N, T * n_h, H, d_k]  the n_h writes of a token on consecutive rows
+ *   v             [N, T * n_h, H, d_v]
+ *   beta          [N, T * n_h, H] fp32
+ *   g             NULL (DeltaNet), [N, T, H] fp32 (one log decay per token and head)
+ *                 or [N, T, H, d_k] fp32 (one per key channel)
+ *   n_h           writes per token, 1 .. 1024 (with or without g)
+ *   state         [M, H, d_k, d_v] fp32, read and written in place; rows that no
+ *                 request names stay as they are, and so does a named row where T is 0
+ *   slot_idx      int32 [N] device array: the state row of each request; NULL:
+ *                 request n uses row n (then M == N).  -1 marks a padding request: no
+ *                 state is touched and its rows of out are zero.  Every other index
+ *                 must lie in 0 .. M-1 and be named once.  A request whose index is
+ *                 out of range, or was named by an earlier request of the call, is
+ *                 handled like a padding request and DN_ERR_SLOTS is reported by
+ *                 deltanet_get_error.
+ *   out           [N, T, H, d_v], dtype of q; fully overwritten
+ *
+ * Supported head dims: d_k, d_v in {64, 128}, bf16 and fp32.  N, T or H may be 0.
+ * The state stays in registers for all T tokens and is read and written once.
+ * Layout rules as deltanet_fwd; state rows may not overlap each other.  state and
+ * out may not overlap each other or any input (DN_ERR_ALIAS).  With
+ * slot_idx the call uses its stream's error word, which the first such call on a
+ * stream allocates: make that call before a capture (inside one it returns
+ * DN_ERR_WORKSPACE, and the capture goes on).  Calls that overlap on the GPU may
+ * not name the same rows.
+ */
+dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor* v,
+                        const dn_tensor* beta, const dn_tensor* g, int n_h, dn_tensor* state,
+                        const dn_tensor* slot_idx, dn_tensor* out, void* stream);
+
+/*
+ * deltanet_scan_fwd -- the gated linear recurrence, channel by channel, over whole
+ * sequences: starting from h_0 = initial_state[n] (or zero),
+ *
+ *     h_t = a_t h_{t-1} + x_t,   a_t = exp(g_t)
+ *
+ * (the recurrence that the matrix-state forms run on each entry of their state,
+ * here with a decay and an input per channel).  A run of tokens is the map
+ * h -> A h + H with A the product of its decays; runs compose exactly, which is how
+ * a sequence is split across warps and CTAs.
+ *
+ *   x             [B, T, D]   bf16 or fp32
+ *   g             [B, T, D]   fp32, or bf16 with bf16 x: ln a.  Any value but NaN and
+ *                             +inf makes sense; -inf is a = 0 (the channel forgets).
+ *   initial_state [N, D] fp32, or NULL for zeros
+ *   cu_seqlens    as deltanet_fwd (B must be 1), or NULL
+ *   out           [B, T, D], dtype of x: h_t rounded to nearest-even
+ *   final_state   [N, D] fp32 (the unrounded h after the last token; initial_state
+ *                 for a sequence without tokens), or NULL
+ *
+ * D is any size >= 1; the last stride of every tensor is 1, other strides are any
+ * non-negative numbers, data aligned to its element.  Aligned and even rows move in
+ * wider pieces.  Outputs may be interleaved views of one buffer (rows side by side,
+ * equal strides); any other overlap of an output is DN_ERR_ALIAS.  No workspace; with
+ * cu_seqlens the call uses its stream's error word (see deltanet_step).  With
+ * cu_seqlens contents that deltanet_get_error reports as DN_ERR_SEQLENS the outputs
+ * are unspecified.  The result does not depend on timing: the same call gives the
+ * same bits.
+ */
+dn_status deltanet_scan_fwd(const dn_tensor* x, const dn_tensor* g,
+                            const dn_tensor* initial_state, const dn_tensor* cu_seqlens,
+                            dn_tensor* out, dn_tensor* final_state, void* stream);
+
+/*
+ * deltanet_scan_bwd -- gradients of deltanet_scan_fwd, from its output.  With
+ * delta_t the gradient of h_t,
+ *
+ *     delta_t = d_out_t + a_{t+1} delta_{t+1}   (last token: d_out + d_final_state)
+ *     d_x_t = delta_t,   d_g_t = delta_t a_t h_{t-1},   d_initial_state = a_1 delta_1
+ *
+ *   g, initial_state, cu_seqlens   as given to the forward call
+ *   out             [B, T, D] the forward call's output: h_{t-1} in d_g is read from
+ *                   it as stored (bf16: rounded, 2^-9 relative in d_g)
+ *   d_out           [B, T, D], dtype of out
+ *   d_final_state   [N, D] fp32, or NULL for zeros
+ *   d_x, d_g        [B, T, D], dtypes of out and g; fully overwritten
+ *   d_initial_state [N, D] fp32, or NULL (not produced)
+ *   other rules as deltanet_scan_fwd.
+ */
+dn_status deltanet_scan_bwd(const dn_tensor* g, const dn_tensor* out,
+                            const dn_tensor* initial_state, const dn_tensor* cu_seqlens,
+                            const dn_tensor* d_out, const dn_tensor* d_final_state,
+                            dn_tensor* d_x, dn_tensor* d_g, dn_tensor* d_initial_state,
+                            void* stream);
+
+/*
+ * deltanet_scan_step -- the gated linear recurrence for the few tokens of a decoding
+ * step, on a cache of states updated in place.
+ *
+ *   x, g       [N, T, D] as deltanet_scan_fwd: T tokens of each request
+ *   state      [M, D] fp32, read and written in place
+ *   slot_idx   as deltanet_step
+ *   out        [N, T, D], dtype of x; fully overwritten (padding requests: zero)
+ *   other rules as deltanet_scan_fwd and, for the cache, as deltanet_step.
+ */
+dn_status deltanet_scan_step(const dn_tensor* x, const dn_tensor* g, dn_tensor* state,
+                             const dn_tensor* slot_idx, dn_tensor* out, void* stream);
+
+/*
+ * deltanet_norm_fwd -- the norms before and after a token-mixing block, fused with
+ * the block's output gate and its scaled residual sum.  Row by row, each part only
+ * where its operand is given:
+ *
+ *     y1 = y rsqrt(mean(y^2) + eps) weight      (else y)
+ *     y2 = y1 act(gate)                         (else y1)
+ *     r' = residual + scale y2                  (scale: else 1)
+ *     n  = r' rsqrt(mean(r'^2) + eps) next_weight
+ *
+ * Without residual, out = y2 (a mixer's heads under their norm and gate, the norm
+ * ahead of a block, or, with weight d^-1/2 and eps / d, the L2 norm of q and k).
+ * With it, residual_out = r', and with next_weight out = n, the next block's input.
+ *
+ *   y, gate, out            [.., d] (2 to 4 dimensions), bf16 or fp32, one dtype
+ *   residual, residual_out  [.., d], the dtype of y, or fp32
+ *   weight, scale, next_weight   [d], bf16 or fp32 each
+ *   activation  DN_ACT_SILU (z / (1 + e^-z)) or DN_ACT_SIGMOID, of the gate
+ *   eps         finite, >= 0
+ *   out         required without residual and with next_weight, NULL otherwise
+ *   residual_out  required with residual, NULL otherwise
+ *
+ * At least one of weight, gate and residual is given; scale and next_weight need
+ * residual.  1 <= d <= 16384 (DN_ERR_UNSUPPORTED above).  Last strides are 1, others
+ * any non-negative numbers, data aligned to its element.  All arithmetic is fp32 and
+ * rounded once per output (n comes from the unrounded r').  Outputs may be
+ * interleaved views of one buffer; any other overlap of an output is DN_ERR_ALIAS.
+ * No workspace and no error word: any call may be captured.
+ */
+enum { DN_ACT_SILU = 0, DN_ACT_SIGMOID = 1 };
+dn_status deltanet_norm_fwd(const dn_tensor* y, const dn_tensor* weight, const dn_tensor* gate,
+                            int activation, const dn_tensor* residual, const dn_tensor* scale,
+                            const dn_tensor* next_weight, float eps, dn_tensor* out,
+                            dn_tensor* residual_out, void* stream);
+
+/*
+ * deltanet_norm_bwd -- gradients of deltanet_norm_fwd from the forward call's inputs
+ * (nothing but them has to be kept).
+ *
+ *   y .. eps         as given to the forward call
+ *   d_out            gradient of out, required where the forward call has an out
+ *   d_residual_out   gradient of residual_out; required with residual, or NULL for zeros
+ *                    where next_weight is given
+ *   d_y, d_gate, d_residual   like y, gate, residual; d_weight, d_scale, d_next_weight
+ *                    [d] fp32; each required where its operand is given, NULL otherwise
+ *   workspace        fp32 [>= deltanet_norm_workspace(rows, d)], contiguous, 16-byte
+ *                    aligned, required where weight, scale or next_weight is given: partial sums
+ *                    over the rows (rows = the product of y's leading dimensions).  Its
+ *                    contents mean nothing before or after the call; calls that may
+ *                    overlap on the GPU need one each.
+ *
+ * The sums over the rows are added in a fixed order: the same call gives the same bits.
+ */
+dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const dn_tensor* gate,
+                            int activation, const dn_tensor* residual, const dn_tensor* scale,
+                            const dn_tensor* next_weight, float eps, const dn_tensor* d_out,
+                            const dn_tensor* d_residual_out, dn_tensor* d_y, dn_tensor* d_weight,
+                            dn_tensor* d_gate, dn_tensor* d_residual, dn_tensor* d_scale,
+                            dn_tensor* d_next_weight, dn_tensor* workspace, void* stream);
+
+/* fp32 elements of deltanet_norm_bwd's workspace for `rows` rows of length d. */
+int64_t deltanet_norm_workspace(int64_t rows, int64_t d);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* deltanet_status_string(dn_status status);
 
 /*
  * deltanet_get_error -- synchronises `stream`, then returns and clears the
- * device-side error flag of the calls made on it (DN_OK, DN_ERR_SEQLENS or
- * DN_ERR_TIMEOUT), or DN_ERR_CUDA if the stream itself reports an error.
+ * device-side error flag of the calls made on it (DN_OK, DN_ERR_SEQLENS,
+ * DN_ERR_TIMEOUT or DN_ERR_SLOTS), or DN_ERR_CUDA if the stream itself reports an error.
  * It also reads and clears the error word of deltanet_fwd_noalloc's scratch
  * on the current device (one per device, shared by all streams).
  */
