@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <initializer_list>
 
 #include "../../include/deltanet.h"
@@ -172,6 +173,73 @@ dn_status scan_common(ScanParams& p, const dn_tensor* x, const dn_tensor* g, con
     return DN_OK;
 }
 
+// Pairs of channels can move as one access: even D, strides and addresses.
+bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
+    auto ok = [](const void* a, int64_t sb, int64_t st, int32_t dt) {
+        return reinterpret_cast<uintptr_t>(a) % (2 * elem_size(dt)) == 0 && sb % 2 == 0 && st % 2 == 0;
+    };
+    return p.D % 2 == 0 && ok(p.x, p.x_sb, p.x_st, x) && ok(p.g, p.g_sb, p.g_st, g) &&
+           ok(p.y, p.y_sb, p.y_st, x) && (!bwd || (ok(p.h, p.h_sb, p.h_st, x) && ok(p.dg, p.dg_sb, p.dg_st, g)));
+}
+
+// CTAs per cluster: enough for two on every SM, while each has tokens.
+int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
+    if (const char* e = getenv("DN_SCAN_K")) return atoi(e);
+    int K = 1;
+    while (K < 8 && items * K < 2 * sms && (int64_t)K * tokens < T) K *= 2;
+    return K;
+}
+
+template <typename Kern>
+dn_status scan_launch(Kern* kern, const ScanParams& p, int64_t items, int K, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * K));
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)K;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = K > 1 ? 1 : 0;
+    if (K > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return DN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, p, K) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
+}
+
+constexpr int kScanTs = 8;         // tokens of a warp's run
+constexpr int kScanSerialT = 32;   // up to so many tokens, one thread walks a channel
+
+template <typename X, typename G, int V, bool PACKED, bool BWD>
+dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
+    const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 32 * V - 1) / (32 * V));
+    const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
+    if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
+    if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, p, items, K, stream);
+    else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, p, items, K, stream);
+}
+
+template <bool BWD>
+dn_status scan_run(const ScanParams& p, int32_t x, int32_t g, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    dn_status st = dn_device_check(dev, sms);
+    if (st != DN_OK) return st;
+    by_types(x, g, [&](auto xt, auto gt) {
+        using X = decltype(xt);
+        using G = decltype(gt);
+        if (p.T <= kScanSerialT) {
+            const unsigned grid = (unsigned)((int64_t)p.N * ((p.D + kScanThreads - 1) / kScanThreads));
+            if constexpr (BWD) k_scan_bwd_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
+            else k_scan_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
+        } else if (scan_pairs(p, x, g, BWD)) {
+            st = p.cu ? scan_tiled<X, G, 2, true, BWD>(p, sms, stream) : scan_tiled<X, G, 2, false, BWD>(p, sms, stream);
+        } else {
+            st = p.cu ? scan_tiled<X, G, 1, true, BWD>(p, sms, stream) : scan_tiled<X, G, 1, false, BWD>(p, sms, stream);
+        }
+    });
+    return st == DN_OK ? launched(1) : st;
+}
+
 template <typename P>
 void set_state(const dn_tensor* t, P*& ptr, int64_t& stride) {
     if (t && numel(t)) {
@@ -334,11 +402,7 @@ dn_status deltanet_scan_fwd(const dn_tensor* x, const dn_tensor* g, const dn_ten
     p.y = out->data; p.y_sb = out->stride[0]; p.y_st = out->stride[1];
     set_state(initial_state, p.s0, p.s0_sn);
     set_state(final_state, p.fin, p.fin_sn);
-    const unsigned grid = (unsigned)(N * ((D + kScanThreads - 1) / kScanThreads));
-    by_types(x->dtype, g->dtype, [&](auto xt, auto gt) {
-        k_scan_serial<decltype(xt), decltype(gt)><<<grid, kScanThreads, 0, stream>>>(p);
-    });
-    return launched(1);
+    return scan_run<false>(p, x->dtype, g->dtype, stream);
 }
 
 dn_status deltanet_scan_bwd(const dn_tensor* g, const dn_tensor* out, const dn_tensor* initial_state,
@@ -368,11 +432,7 @@ dn_status deltanet_scan_bwd(const dn_tensor* g, const dn_tensor* out, const dn_t
     set_state(initial_state, p.s0, p.s0_sn);
     set_state(d_final_state, p.sT, p.sT_sn);
     set_state(d_initial_state, p.fin, p.fin_sn);
-    const unsigned grid = (unsigned)(N * ((D + kScanThreads - 1) / kScanThreads));
-    by_types(out->dtype, g->dtype, [&](auto xt, auto gt) {
-        k_scan_bwd_serial<decltype(xt), decltype(gt)><<<grid, kScanThreads, 0, stream>>>(p);
-    });
-    return launched(1);
+    return scan_run<true>(p, out->dtype, g->dtype, stream);
 }
 
 dn_status deltanet_scan_step(const dn_tensor* x, const dn_tensor* g, dn_tensor* state,

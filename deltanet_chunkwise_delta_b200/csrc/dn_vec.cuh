@@ -41,6 +41,44 @@ __device__ __forceinline__ void st_elem4(E* p, float4 x) {
     }
 }
 
+// V = 1 or 2 consecutive elements as loaded (2: one 4- or 8-byte access), to and from fp32.
+template <typename E, int V> struct RawVec;
+template <> struct RawVec<__nv_bfloat16, 1> { using T = unsigned short; };
+template <> struct RawVec<__nv_bfloat16, 2> { using T = uint32_t; };
+template <> struct RawVec<float, 1> { using T = float; };
+template <> struct RawVec<float, 2> { using T = float2; };
+
+__device__ __forceinline__ void unpack(unsigned short r, float* f) { f[0] = __uint_as_float((uint32_t)r << 16); }
+__device__ __forceinline__ void unpack(uint32_t r, float* f) {
+    f[0] = __uint_as_float(r << 16);
+    f[1] = __uint_as_float(r & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(float r, float* f) { f[0] = r; }
+__device__ __forceinline__ void unpack(float2 r, float* f) {
+    f[0] = r.x;
+    f[1] = r.y;
+}
+__device__ __forceinline__ void pack(const float* f, unsigned short& r) {
+    r = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+}
+__device__ __forceinline__ void pack(const float* f, uint32_t& r) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[0], f[1]);
+    r = *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void pack(const float* f, float& r) { r = f[0]; }
+__device__ __forceinline__ void pack(const float* f, float2& r) { r = make_float2(f[0], f[1]); }
+
+template <typename E, int V>
+__device__ __forceinline__ typename RawVec<E, V>::T ld_raw(const E* p) {
+    return *reinterpret_cast<const typename RawVec<E, V>::T*>(p);
+}
+template <typename E, int V>
+__device__ __forceinline__ void st_vec(E* p, const float* f) {
+    typename RawVec<E, V>::T r;
+    pack(f, r);
+    *reinterpret_cast<typename RawVec<E, V>::T*>(p) = r;
+}
+
 // A [d] parameter vector in fp32 or bf16.
 struct ParamVec {
     const void* p;  // null: not given
