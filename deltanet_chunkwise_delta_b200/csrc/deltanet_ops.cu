@@ -190,11 +190,12 @@ int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
     return K;
 }
 
-template <typename Kern>
-dn_status scan_launch(Kern* kern, const ScanParams& p, int64_t items, int K, cudaStream_t stream) {
+template <typename Kern, typename... A>
+dn_status scan_launch(Kern* kern, int64_t items, int K, int smem, cudaStream_t stream, const ScanParams& p, A... a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * K));
     cfg.blockDim = dim3(kScanThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -202,21 +203,42 @@ dn_status scan_launch(Kern* kern, const ScanParams& p, int64_t items, int K, cud
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = K > 1 ? 1 : 0;
-    if (K > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    if (smem > 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return DN_ERR_CUDA;
-    return cudaLaunchKernelEx(&cfg, kern, p, K) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, p, K, a...) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
 }
 
-constexpr int kScanTs = 8;         // tokens of a warp's run
+constexpr int kScanTs = 8;         // tokens of a warp's run (one channel a lane)
 constexpr int kScanSerialT = 32;   // up to so many tokens, one thread walks a channel
+
+// 16-byte copies: bit 0 for x, 1 for g, 2 for h.
+int scan_wide(const ScanParams& p, int32_t x, int32_t g) {
+    auto ok = [](const void* a, int64_t sb, int64_t st, int32_t dt) {
+        const int64_t es = elem_size(dt);
+        return aligned16(a) && sb * es % 16 == 0 && st * es % 16 == 0;
+    };
+    return (ok(p.x, p.x_sb, p.x_st, x) ? 1 : 0) | (ok(p.g, p.g_sb, p.g_st, g) ? 2 : 0) |
+           (p.h && ok(p.h, p.h_sb, p.h_st, x) ? 4 : 0);
+}
 
 template <typename X, typename G, int V, bool PACKED, bool BWD>
 dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 32 * V - 1) / (32 * V));
-    const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
-    if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-    if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, p, items, K, stream);
-    else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, p, items, K, stream);
+    if constexpr (V == 2) {
+        // fp32 rows: half the tokens, for the same bytes on their way
+        constexpr int TS = sizeof(X) == 4 ? 4 : 8;
+        constexpr int smem = (int)sizeof(ScanStage<X, G, TS, BWD>);
+        const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
+        const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
+        if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
+        if constexpr (BWD) return scan_launch(k_scan_bwd_piped<X, G, TS, PACKED>, items, K, smem, stream, p, wide);
+        else return scan_launch(k_scan_piped<X, G, TS, PACKED>, items, K, smem, stream, p, wide);
+    } else {
+        const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
+        if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
+        if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, items, K, 0, stream, p);
+        else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, items, K, 0, stream, p);
+    }
 }
 
 template <bool BWD>

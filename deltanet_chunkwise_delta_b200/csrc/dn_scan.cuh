@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_serial(ScanParams p) 
 // passes H on whatever comes in, so that nothing of another sequence, NaN included, leaks:
 // A = -1 marks it (products of decays are >= 0).
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanMaxCluster = 16;
+constexpr int kScanMaxCluster = 8;
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -433,6 +433,458 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd_tiled(ScanParams p
     if (!PACKED && p.fin && live && rank == 0 && w == 0)
 #pragma unroll
         for (int v = 0; v < V; ++v) p.fin[b * p.fin_sn + c + v] = carry[v];
+}
+
+// ---- pairs of channels: tokens staged in shared memory ------------------------------------
+//
+// The same split with two channels per lane and the tokens of three tiles on their way
+// through shared memory (cp.async; a warp reads only what it copied itself).  The (A, H) of
+// tile i + 1 are formed and sent before tile i is finished, so that the cluster's barrier
+// passes behind that work; a tile is finished by running its recurrence again from the h that
+// comes in (the decays of an fp32 gate are left in its place in shared memory by the first
+// pass; of a bf16 gate the exponential is taken twice).
+constexpr int kScanStages = 3;
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+// the first n bytes from src, zeros after
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Copies rows j = 0 .. TS - 1 (token t + DIR * j; zeros outside 0 .. T - 1 and past channel D)
+// of 64 channels from channel c0 with one warp, 64 elements a row: 16 bytes a lane where
+// addresses allow, else a lane's own pair.
+template <typename E, int TS, int DIR>
+struct ScanSrc {
+    static constexpr int kPer = 64 * sizeof(E) / 16;        // lanes of a row at 16 bytes each
+    const E* base;                                          // this lane's piece of token 0
+    int64_t st, inc;
+    int row, left;                                          // its first row; bytes of the piece that exist
+    bool wide;
+    __device__ __forceinline__ ScanSrc(const E* p, int64_t st_, int c0, int D, bool wide_) : st(st_), wide(wide_) {
+        const int lane = threadIdx.x & 31, bytes = wide ? 16 : 2 * (int)sizeof(E);
+        row = wide ? lane / kPer : 0;
+        const int c = c0 + (wide ? lane % kPer * (16 / (int)sizeof(E)) : lane * 2);
+        left = max(0, min(bytes, (D - c) * (int)sizeof(E)));
+        base = left ? p + c : p;
+        inc = DIR * st * (wide ? 32 / kPer : 1);
+    }
+    __device__ __forceinline__ void copy(E* dst, int64_t t, int T, bool inside) const {
+        const int lane = threadIdx.x & 31;
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+        const E* src = base + (t + DIR * row) * st;
+        if (wide) {
+            if (inside) {
+#pragma unroll
+                for (int i = 0; i < TS * kPer / 32; ++i, src += inc) cp_async<16>(d + i * 512 + lane * 16, src);
+            } else {
+#pragma unroll
+                for (int i = 0; i < TS * kPer / 32; ++i, src += inc) {
+                    const int64_t tt = t + DIR * (row + i * (32 / kPer));
+                    const bool in = tt >= 0 && tt < T;
+                    cp_async<16>(d + i * 512 + lane * 16, in ? src : base, in ? left : 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < TS; ++j, src += inc) {
+                const bool in = t + DIR * j >= 0 && t + DIR * j < T;
+                cp_async<2 * (int)sizeof(E)>(d + (j * 64 + lane * 2) * (int)sizeof(E), in ? src : base, in ? left : 0);
+            }
+        }
+    }
+};
+
+// e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
+// relative in all, where a token's step needs no more: a decay's error enters h with weight a.
+__device__ __forceinline__ float scan_log2(float g) { return g * 1.44269504f; }
+__device__ __forceinline__ float scan_pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct ScanRuns {
+    float4 warp[2][kScanWarps][32];       // (A0, A1, H0, H1) of each warp's run, by tile parity
+    float4 cta[2][kScanMaxCluster][32];   // of each CTA's run
+};
+
+// The product of a run's decays from the sum of their logarithms (base 2), kept below infinity.
+__device__ __forceinline__ float run_decay(float l) { return scan_pow2(fminf(l, 127.f)); }
+
+template <bool PACKED>
+__device__ __forceinline__ void run_through(float4 r, float& c0, float& c1) {
+    c0 = run_map<PACKED>(r.x, r.z, c0);
+    c1 = run_map<PACKED>(r.y, r.w, c1);
+}
+// r after q
+template <bool PACKED>
+__device__ __forceinline__ float4 run_join(float4 r, float4 q) {
+    return make_float4(run_prod<PACKED>(r.x, q.x), run_prod<PACKED>(r.y, q.y), run_map<PACKED>(r.x, r.z, q.z),
+                       run_map<PACKED>(r.y, r.w, q.w));
+}
+
+// The exchange of one tile in two halves.  send: this warp's run out, the run of the warps
+// before it into `pre`; receive (after send of the same tile by all): what comes into this
+// warp's run into cin, what leaves the tile into carry.
+template <bool PACKED>
+__device__ __forceinline__ void runs_send(ScanRuns& sm, int par, int K, unsigned rank, float4 run, float4& pre) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    sm.warp[par][w][lane] = run;
+    __syncthreads();
+    if (K == 1) return;
+    pre = make_float4(1.f, 1.f, 0.f, 0.f);
+    for (int i = 0; i < w; ++i) pre = run_join<PACKED>(sm.warp[par][i][lane], pre);
+    if (w == kScanWarps - 1) {
+        const float4 all = run_join<PACKED>(run, pre);
+        const uint32_t a = (uint32_t)__cvta_generic_to_shared(&sm.cta[par][rank][lane]);
+        for (int r = 0; r < K; ++r) {
+            uint32_t b;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(r));
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(b), "f"(all.x), "f"(all.y),
+                         "f"(all.z), "f"(all.w) : "memory");
+        }
+    }
+    cluster_arrive();
+}
+template <bool PACKED>
+__device__ __forceinline__ void runs_receive(ScanRuns& sm, int par, int K, unsigned rank, float4 pre, float* carry,
+                                             float* cin) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (K == 1) {
+#pragma unroll
+        for (int i = 0; i < kScanWarps; ++i) {
+            if (i == w) cin[0] = carry[0], cin[1] = carry[1];
+            run_through<PACKED>(sm.warp[par][i][lane], carry[0], carry[1]);
+        }
+        return;
+    }
+    cluster_wait();
+    for (int r = 0; r < K; ++r) {
+        if (r == (int)rank) cin[0] = carry[0], cin[1] = carry[1];
+        run_through<PACKED>(sm.cta[par][r][lane], carry[0], carry[1]);
+    }
+    run_through<PACKED>(pre, cin[0], cin[1]);
+}
+
+// Packed input: which of a warp's tokens start or end a sequence.  (lo, hi) is the last
+// sequence looked up; tokens well inside it need no search.
+struct ScanSeq {
+    int lo = 0, hi = 0;
+    unsigned starts = 0, ends = 0;
+    template <int TS, int DIR>
+    __device__ __forceinline__ void find(const ScanParams& p, int64_t t0) {
+        const int64_t a = DIR > 0 ? t0 : t0 - (TS - 1), b = a + TS;    // tokens [a, b)
+        starts = ends = 0;
+        if (a > lo && b < hi) return;
+        const int lane = threadIdx.x & 31;
+        const int64_t tl = t0 + DIR * (lane < TS ? lane : TS - 1);
+        const int t = (int)(tl < 0 ? 0 : tl < p.T ? tl : p.T - 1);
+        const int n = scan_owner(p.cu, p.N, t);
+        const bool in = lane < TS && tl >= 0 && tl < p.T;
+        const int s = p.cu[n], e = p.cu[n + 1];
+        starts = __ballot_sync(~0u, in && s == t);
+        ends = __ballot_sync(~0u, in && e == t + 1);
+        lo = __shfl_sync(~0u, s, TS - 1);
+        hi = __shfl_sync(~0u, e, TS - 1);
+    }
+};
+
+// The tokens on their way, a warp's rows together.  h is read only when a tile is finished,
+// one tile later than x and g: two stages of it are enough.
+template <typename X, typename G, int TS, bool BWD>
+struct ScanStage {
+    G g[kScanStages][kScanWarps][TS][64];
+    X x[kScanStages][kScanWarps][TS][64];
+    X h[BWD ? 2 : 1][BWD ? kScanWarps : 1][BWD ? TS : 1][64];
+};
+
+template <typename X, typename G, int TS, bool PACKED>
+__global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K, int wide) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    ScanStage<X, G, TS, false>& st = *reinterpret_cast<ScanStage<X, G, TS, false>*>(dyn);
+    __shared__ ScanRuns sm;
+    const unsigned rank = K > 1 ? cluster_rank() : 0;
+    const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
+    const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = (item % ct) * 64, c = c0 + lane * 2;
+    const bool live = c < p.D, whole = c0 + 64 <= p.D;
+    const ScanSrc<X, TS, 1> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, c0, p.D, wide & 1);
+    const ScanSrc<G, TS, 1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, c0, p.D, wide & 2);
+    X* y = static_cast<X*>(p.y) + b * p.y_sb + c;
+    const int step = K * kScanWarps * TS;
+    const int tiles = (int)(((int64_t)p.T + step - 1) / step);
+    int64_t t0 = ((int64_t)rank * kScanWarps + w) * TS;      // this warp's first token of tile i
+    auto load = [&](int64_t t, int s) {
+        const bool inside = whole && t + TS <= p.T;
+        xs.copy(&st.x[s][w][0][0], t, p.T, inside);
+        gs.copy(&st.g[s][w][0][0], t, p.T, inside);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kScanStages; ++s) load(t0 + (int64_t)s * step, s);
+    if (PACKED) {
+        scan_check_cu(p);
+        scan_empty<2>(p, p.s0, p.s0_sn, c, K, rank);
+    }
+    float carry[2] = {0.f, 0.f}, cin[2];
+    if (!PACKED && live && p.s0) {
+        carry[0] = p.s0[b * p.s0_sn + c];
+        carry[1] = p.s0[b * p.s0_sn + c + 1];
+    }
+    auto initial = [&](int64_t t, float* s) {      // the start state of the sequence that t starts
+        const int n = scan_owner(p.cu, p.N, (int)t);
+        s[0] = live && p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
+        s[1] = live && p.s0 ? p.s0[n * p.s0_sn + c + 1] : 0.f;
+    };
+    // the run of this warp's tokens of one tile
+    auto form = [&](int64_t t, int s, unsigned starts) {
+        float h[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            float xv[2], a[2];
+            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
+            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float l = scan_log2(a[v]);
+                L[v] += l;
+                a[v] = scan_pow2(l);
+            }
+            if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
+            if (PACKED && (starts >> j & 1)) initial(t + j, h);
+            h[0] = fmaf(a[0], h[0], xv[0]);
+            h[1] = fmaf(a[1], h[1], xv[1]);
+        }
+        return PACKED && starts ? make_float4(-1.f, -1.f, h[0], h[1])
+                                : make_float4(run_decay(L[0]), run_decay(L[1]), h[0], h[1]);
+    };
+    // the same tokens again from what comes in, to the output
+    auto finish = [&](int64_t t, int s, unsigned starts, unsigned ends) {
+        const int left = (int)min((int64_t)TS, p.T - t);
+        X* o = y + t * p.y_st;
+#pragma unroll
+        for (int j = 0; j < TS; ++j, o += p.y_st) {
+            float xv[2], a[2];
+            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
+            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+            if constexpr (sizeof(G) == 2) {
+                a[0] = scan_pow2(scan_log2(a[0]));
+                a[1] = scan_pow2(scan_log2(a[1]));
+            }
+            if (PACKED && (starts >> j & 1)) initial(t + j, cin);
+            cin[0] = fmaf(a[0], cin[0], xv[0]);
+            cin[1] = fmaf(a[1], cin[1], xv[1]);
+            if (live && j < left) st_vec<X, 2>(o, cin);
+            if (PACKED && (ends >> j & 1) && live && p.fin) {
+                float* f = p.fin + scan_owner(p.cu, p.N, (int)(t + j)) * p.fin_sn + c;
+                f[0] = cin[0];
+                f[1] = cin[1];
+            }
+        }
+        // the places past the last token hold a = 1, x = 0: they leave h as it is
+        if (!PACKED && left > 0 && t + TS >= p.T && live && p.fin) {
+            p.fin[b * p.fin_sn + c] = cin[0];
+            p.fin[b * p.fin_sn + c + 1] = cin[1];
+        }
+    };
+    if (K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    ScanSeq seq;
+    float4 pre = make_float4(1.f, 1.f, 0.f, 0.f);
+    auto next = [&](int64_t t, int s, int par) {   // forms and sends the run of a tile that has landed
+        __syncwarp();
+        float4 run;
+        if (PACKED) {
+            seq.find<TS, 1>(p, t);
+            run = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
+        } else {
+            run = form(t, s, 0u);
+        }
+        runs_send<PACKED>(sm, par, K, rank, run, pre);
+    };
+    static_assert(kScanStages == 3, "the waits count the tiles behind the one wanted");
+    if (tiles > 0) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        next(t0, 0, 0);
+    }
+    int s = 0;
+    for (int i = 0; i < tiles; ++i, t0 += step) {
+        runs_receive<PACKED>(sm, i & 1, K, rank, pre, carry, cin);
+        const unsigned starts = seq.starts, ends = seq.ends;
+        const int s1 = s + 1 == kScanStages ? 0 : s + 1;
+        if (i + 1 < tiles) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            next(t0 + step, s1, (i + 1) & 1);
+        }
+        if (PACKED && (starts | ends)) finish(t0, s, starts, ends);
+        else finish(t0, s, 0u, 0u);
+        __syncwarp();
+        load(t0 + (int64_t)kScanStages * step, s);
+        s = s1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!PACKED && p.T == 0 && p.fin && live && rank == 0 && w == 0) {
+        p.fin[b * p.fin_sn + c] = carry[0];
+        p.fin[b * p.fin_sn + c + 1] = carry[1];
+    }
+}
+
+template <typename X, typename G, int TS, bool PACKED>
+__global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, int K, int wide) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    ScanStage<X, G, TS, true>& st = *reinterpret_cast<ScanStage<X, G, TS, true>*>(dyn);
+    __shared__ ScanRuns sm;
+    const unsigned rank = K > 1 ? cluster_rank() : 0;
+    const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
+    const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = (item % ct) * 64, c = c0 + lane * 2;
+    const bool live = c < p.D, whole = c0 + 64 <= p.D;
+    const ScanSrc<X, TS, -1> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, c0, p.D, wide & 1);
+    const ScanSrc<G, TS, -1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, c0, p.D, wide & 2);
+    const ScanSrc<X, TS, -1> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, c0, p.D, wide & 4);
+    X* dx = static_cast<X*>(p.y) + b * p.y_sb + c;
+    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c;
+    const int step = K * kScanWarps * TS;
+    const int tiles = (int)(((int64_t)p.T + step - 1) / step);
+    int64_t t0 = p.T - 1 - ((int64_t)rank * kScanWarps + w) * TS;    // token of place j of tile i: t0 - j
+    auto load = [&](int64_t t, int s) {
+        const bool inside = whole && t >= TS - 1;
+        ds.copy(&st.x[s][w][0][0], t, p.T, inside);
+        gs.copy(&st.g[s][w][0][0], t, p.T, inside);
+    };
+    auto load_h = [&](int64_t t, int i) { hs.copy(&st.h[i & 1][w][0][0], t - 1, p.T, whole && t >= TS); };
+#pragma unroll
+    for (int s = 0; s < kScanStages; ++s) {
+        load(t0 - (int64_t)s * step, s);
+        if (s < 2) load_h(t0 - (int64_t)s * step, s);
+        cp_async_commit();
+    }
+    if (PACKED) {
+        scan_check_cu(p);
+        scan_empty<2>(p, p.sT, p.sT_sn, c, K, rank);
+    }
+    float carry[2] = {0.f, 0.f}, cin[2];
+    if (!PACKED && live && p.sT) {
+        carry[0] = p.sT[b * p.sT_sn + c];
+        carry[1] = p.sT[b * p.sT_sn + c + 1];
+    }
+    auto state = [&](const float* src, int64_t sn, int n, float* s) {
+        s[0] = live && src ? src[n * sn + c] : 0.f;
+        s[1] = live && src ? src[n * sn + c + 1] : 0.f;
+    };
+    auto form = [&](int64_t t, int s, unsigned ends) {
+        float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            float dv[2], a[2];
+            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), dv);
+            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float l = scan_log2(a[v]);
+                L[v] += l;
+                a[v] = scan_pow2(l);
+            }
+            if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
+            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, scan_owner(p.cu, p.N, (int)(t - j)), e);
+            e[0] = a[0] * (dv[0] + e[0]);
+            e[1] = a[1] * (dv[1] + e[1]);
+        }
+        return PACKED && ends ? make_float4(-1.f, -1.f, e[0], e[1])
+                              : make_float4(run_decay(L[0]), run_decay(L[1]), e[0], e[1]);
+    };
+    auto finish = [&](int64_t t, int s, int hslot, unsigned starts, unsigned ends) {
+        // places up to `left` hold tokens; dense: place left - 1 of the last tile is token 0
+        const int left = (int)max((int64_t)0, min((int64_t)TS, t + 1));
+        const bool at0 = !PACKED && left > 0 && t < TS;
+        X* ox = dx + t * p.y_st;
+        G* og = dg + t * p.dg_st;
+#pragma unroll
+        for (int j = 0; j < TS; ++j, ox -= p.y_st, og -= p.dg_st) {
+            float dv[2], a[2], hv[2];
+            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), dv);
+            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+            unpack(ld_raw<X, 2>(&st.h[hslot][w][j][lane * 2]), hv);
+            if constexpr (sizeof(G) == 2) {
+                a[0] = scan_pow2(scan_log2(a[0]));
+                a[1] = scan_pow2(scan_log2(a[1]));
+            }
+            int n = b;
+            if (PACKED && ((starts | ends) >> j & 1)) n = scan_owner(p.cu, p.N, (int)(t - j));
+            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, n, cin);
+            if (PACKED ? (starts >> j & 1) : at0 && j == left - 1) state(p.s0, p.s0_sn, n, hv);
+            const float d[2] = {dv[0] + cin[0], dv[1] + cin[1]};
+            cin[0] = a[0] * d[0];
+            cin[1] = a[1] * d[1];
+            if (live && j < left) {
+                const float q[2] = {cin[0] * hv[0], cin[1] * hv[1]};
+                st_vec<X, 2>(ox, d);
+                st_vec<G, 2>(og, q);
+            }
+            if (PACKED && (starts >> j & 1) && live && p.fin) {
+                p.fin[n * p.fin_sn + c] = cin[0];
+                p.fin[n * p.fin_sn + c + 1] = cin[1];
+            }
+        }
+        // the places past token 0 hold a = 1, d = 0: they leave what comes in as it is
+        if (at0 && live && p.fin) {
+            p.fin[b * p.fin_sn + c] = cin[0];
+            p.fin[b * p.fin_sn + c + 1] = cin[1];
+        }
+    };
+    if (K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    ScanSeq seq;
+    float4 pre = make_float4(1.f, 1.f, 0.f, 0.f);
+    auto next = [&](int64_t t, int s, int par) {
+        __syncwarp();
+        float4 run;
+        if (PACKED) {
+            seq.find<TS, -1>(p, t);
+            run = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
+        } else {
+            run = form(t, s, 0u);
+        }
+        runs_send<PACKED>(sm, par, K, rank, run, pre);
+    };
+    if (tiles > 0) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        next(t0, 0, 0);
+    }
+    int s = 0;
+    for (int i = 0; i < tiles; ++i, t0 -= step) {
+        runs_receive<PACKED>(sm, i & 1, K, rank, pre, carry, cin);
+        const unsigned starts = seq.starts, ends = seq.ends;
+        const int s1 = s + 1 == kScanStages ? 0 : s + 1;
+        if (i + 1 < tiles) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            next(t0 - step, s1, (i + 1) & 1);
+        }
+        if (PACKED && (starts | ends)) finish(t0, s, i & 1, starts, ends);
+        else finish(t0, s, i & 1, 0u, 0u);
+        __syncwarp();
+        load(t0 - (int64_t)kScanStages * step, s);
+        load_h(t0 - 2 * (int64_t)step, i);
+        cp_async_commit();
+        s = s1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!PACKED && p.T == 0 && p.fin && live && rank == 0 && w == 0) {
+        p.fin[b * p.fin_sn + c] = carry[0];
+        p.fin[b * p.fin_sn + c + 1] = carry[1];
+    }
 }
 
 struct ScanStepParams {
