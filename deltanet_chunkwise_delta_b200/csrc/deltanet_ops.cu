@@ -144,6 +144,7 @@ dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* c
     const int64_t B = x->shape[0], T = x->shape[1], D = x->shape[2];
     if (B < 0 || T < 0 || D < 1 || D > kMax31 || T > kMax31 || B > kMax31) return DN_ERR_INVALID_ARG;
     if (T > 0 && B > kMax31 / T) return DN_ERR_INVALID_ARG;
+    if (T > kMax31 - 4096) return DN_ERR_INVALID_ARG;   // the kernels' token counters run past T by a few tiles
     const int64_t dims[3] = {B, T, D};
     if (!view_ok(x, 3, dims, kF32 | kBf16)) return DN_ERR_INVALID_ARG;
     if (!view_ok(g, 3, dims, x->dtype == DN_F32 ? kF32 : kF32 | kBf16)) return DN_ERR_INVALID_ARG;
@@ -166,11 +167,12 @@ dn_status scan_common(ScanParams& p, const dn_tensor* x, const dn_tensor* g, con
     p.x = x->data; p.x_sb = x->stride[0]; p.x_st = x->stride[1];
     p.g = g->data; p.g_sb = g->stride[0]; p.g_st = g->stride[1];
     p.B = (int)x->shape[0]; p.T = (int)x->shape[1]; p.D = (int)x->shape[2]; p.N = (int)N;
-    if (cu) {
-        p.cu = static_cast<const int*>(cu->data);
-        if ((st = dn_stream_flag(dev, stream, &p.err)) != DN_OK) return st;
-    }
-    return DN_OK;
+    // packed input reports its boundaries through the error word; without it only a wait
+    // inside a cluster that gave up would, and a capture that finds none goes on without
+    st = dn_stream_flag(dev, stream, &p.err);
+    if (!cu) return DN_OK;
+    p.cu = static_cast<const int*>(cu->data);
+    return st;
 }
 
 // Pairs of channels can move as one access: even D, strides and addresses.
@@ -191,10 +193,11 @@ int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
 }
 
 template <typename Kern, typename... A>
-dn_status scan_launch(Kern* kern, int64_t items, int K, int smem, cudaStream_t stream, const ScanParams& p, A... a) {
+dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, cudaStream_t stream,
+                      const ScanParams& p, A... a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * K));
-    cfg.blockDim = dim3(kScanThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at;
@@ -231,13 +234,13 @@ dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
         const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
         const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
         if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-        if constexpr (BWD) return scan_launch(k_scan_bwd_piped<X, G, TS, PACKED>, items, K, smem, stream, p, wide);
-        else return scan_launch(k_scan_piped<X, G, TS, PACKED>, items, K, smem, stream, p, wide);
+        if constexpr (BWD) return scan_launch(k_scan_bwd_piped<X, G, TS, PACKED>, items, K, kScanPipedThreads, smem, stream, p, wide);
+        else return scan_launch(k_scan_piped<X, G, TS, PACKED>, items, K, kScanPipedThreads, smem, stream, p, wide);
     } else {
         const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
         if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-        if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, items, K, 0, stream, p);
-        else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, items, K, 0, stream, p);
+        if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, items, K, kScanThreads, 0, stream, p);
+        else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, items, K, kScanThreads, 0, stream, p);
     }
 }
 

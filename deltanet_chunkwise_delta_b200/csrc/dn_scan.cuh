@@ -3,6 +3,7 @@
 #pragma once
 
 #include "dn_common.cuh"
+#include "dn_sm100.cuh"
 #include "dn_step.cuh"
 #include "dn_vec.cuh"
 
@@ -438,12 +439,15 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd_tiled(ScanParams p
 // ---- pairs of channels: tokens staged in shared memory ------------------------------------
 //
 // The same split with two channels per lane and the tokens of three tiles on their way
-// through shared memory (cp.async; a warp reads only what it copied itself).  The (A, H) of
-// tile i + 1 are formed and sent before tile i is finished, so that the cluster's barrier
-// passes behind that work; a tile is finished by running its recurrence again from the h that
-// comes in (the decays of an fp32 gate are left in its place in shared memory by the first
-// pass; of a bf16 gate the exponential is taken twice).
+// through shared memory (cp.async; a warp reads only what it copied itself).  Eight warps
+// form the (A, H) of tile i + 1 before they finish tile i; a ninth joins the warps' runs,
+// sends the CTA's to the cluster's other CTAs (st.async on their mbarriers), waits for theirs
+// and hands every warp the h before its run, all of it behind the finishing of the tile
+// before.  A tile is finished by running its recurrence again from the h that comes in (the
+// decays of an fp32 gate are left in its place in shared memory by the first pass; of a bf16
+// gate the power is taken twice).
 constexpr int kScanStages = 3;
+constexpr int kScanPipedThreads = kScanThreads + 32;
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
@@ -458,28 +462,32 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Copies rows j = 0 .. TS - 1 (token t + DIR * j; zeros outside 0 .. T - 1 and past channel D)
-// of 64 channels from channel c0 with one warp, 64 elements a row: 16 bytes a lane where
-// addresses allow, else a lane's own pair.
+// Copies the tokens of one warp's run into shared memory, tile after tile: rows j = 0 .. TS - 1
+// (token t + DIR * j; zeros outside 0 .. T - 1 and past channel D) of 64 channels from c0, 64
+// elements a row; 16 bytes a lane where addresses allow, else a lane's own pair.
 template <typename E, int TS, int DIR>
 struct ScanSrc {
     static constexpr int kPer = 64 * sizeof(E) / 16;        // lanes of a row at 16 bytes each
-    const E* base;                                          // this lane's piece of token 0
-    int64_t st, inc;
+    const E* base;                                          // a readable address
+    const E* cur;                                           // this lane's first piece of the tile
+    int64_t inc, tile;                                      // to the lane's next piece, to the next tile
     int row, left;                                          // its first row; bytes of the piece that exist
     bool wide;
-    __device__ __forceinline__ ScanSrc(const E* p, int64_t st_, int c0, int D, bool wide_) : st(st_), wide(wide_) {
+    __device__ __forceinline__ ScanSrc(const E* p, int64_t st, int t, int step, int c0, int D, bool wide_) : wide(wide_) {
         const int lane = threadIdx.x & 31, bytes = wide ? 16 : 2 * (int)sizeof(E);
         row = wide ? lane / kPer : 0;
         const int c = c0 + (wide ? lane % kPer * (16 / (int)sizeof(E)) : lane * 2);
         left = max(0, min(bytes, (D - c) * (int)sizeof(E)));
-        base = left ? p + c : p;
+        base = p;
+        cur = p + c + (t + DIR * row) * st;
         inc = DIR * st * (wide ? 32 / kPer : 1);
+        tile = DIR * st * step;
     }
-    __device__ __forceinline__ void copy(E* dst, int64_t t, int T, bool inside) const {
+    // t: the tile's first token; inside: every row and channel of it exists
+    __device__ __forceinline__ void copy(E* dst, int t, int T, bool inside) {
         const int lane = threadIdx.x & 31;
         const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-        const E* src = base + (t + DIR * row) * st;
+        const E* src = cur;
         if (wide) {
             if (inside) {
 #pragma unroll
@@ -487,18 +495,18 @@ struct ScanSrc {
             } else {
 #pragma unroll
                 for (int i = 0; i < TS * kPer / 32; ++i, src += inc) {
-                    const int64_t tt = t + DIR * (row + i * (32 / kPer));
-                    const bool in = tt >= 0 && tt < T;
+                    const bool in = (unsigned)(t + DIR * (row + i * (32 / kPer))) < (unsigned)T && left > 0;
                     cp_async<16>(d + i * 512 + lane * 16, in ? src : base, in ? left : 0);
                 }
             }
         } else {
 #pragma unroll
             for (int j = 0; j < TS; ++j, src += inc) {
-                const bool in = t + DIR * j >= 0 && t + DIR * j < T;
+                const bool in = (unsigned)(t + DIR * j) < (unsigned)T && left > 0;
                 cp_async<2 * (int)sizeof(E)>(d + (j * 64 + lane * 2) * (int)sizeof(E), in ? src : base, in ? left : 0);
             }
         }
+        cur += tile;
     }
 };
 
@@ -514,6 +522,9 @@ __device__ __forceinline__ float scan_pow2(float x) {
 struct ScanRuns {
     float4 warp[2][kScanWarps][32];       // (A0, A1, H0, H1) of each warp's run, by tile parity
     float4 cta[2][kScanMaxCluster][32];   // of each CTA's run
+    float2 cin[2][kScanWarps][32];        // what comes into each warp's run
+    uint64_t full[2];                     // the cluster's runs of a tile have arrived
+    sm100::WaitCtl ctl;
 };
 
 // The product of a run's decays from the sum of their logarithms (base 2), kept below infinity.
@@ -531,47 +542,84 @@ __device__ __forceinline__ float4 run_join(float4 r, float4 q) {
                        run_map<PACKED>(r.y, r.w, q.w));
 }
 
-// The exchange of one tile in two halves.  send: this warp's run out, the run of the warps
-// before it into `pre`; receive (after send of the same tile by all): what comes into this
-// warp's run into cin, what leaves the tile into carry.
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+constexpr int kBarRuns = 1, kBarCin = 2;   // named barriers: runs of a tile formed, h before them known
+
+// The ninth warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
+// into the first tile, in the end what leaves the last one.
 template <bool PACKED>
-__device__ __forceinline__ void runs_send(ScanRuns& sm, int par, int K, unsigned rank, float4 run, float4& pre) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    sm.warp[par][w][lane] = run;
-    __syncthreads();
-    if (K == 1) return;
-    pre = make_float4(1.f, 1.f, 0.f, 0.f);
-    for (int i = 0; i < w; ++i) pre = run_join<PACKED>(sm.warp[par][i][lane], pre);
-    if (w == kScanWarps - 1) {
-        const float4 all = run_join<PACKED>(run, pre);
-        const uint32_t a = (uint32_t)__cvta_generic_to_shared(&sm.cta[par][rank][lane]);
-        for (int r = 0; r < K; ++r) {
-            uint32_t b;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(r));
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(b), "f"(all.x), "f"(all.y),
-                         "f"(all.z), "f"(all.w) : "memory");
-        }
-    }
-    cluster_arrive();
-}
-template <bool PACKED>
-__device__ __forceinline__ void runs_receive(ScanRuns& sm, int par, int K, unsigned rank, float4 pre, float* carry,
-                                             float* cin) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (K == 1) {
+__device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsigned rank, float* carry, int* err) {
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    for (int i = 0; i < tiles; ++i) {
+        const int par = i & 1;
+        bar_sync(kBarRuns, kScanPipedThreads);
+        if (K == 1) {
 #pragma unroll
-        for (int i = 0; i < kScanWarps; ++i) {
-            if (i == w) cin[0] = carry[0], cin[1] = carry[1];
-            run_through<PACKED>(sm.warp[par][i][lane], carry[0], carry[1]);
+            for (int w = 0; w < kScanWarps; ++w) {
+                sm.cin[par][w][lane] = make_float2(carry[0], carry[1]);
+                run_through<PACKED>(sm.warp[par][w][lane], carry[0], carry[1]);
+            }
+        } else {
+            float4 pre[kScanWarps], all = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kScanWarps; ++w) {
+                pre[w] = all;
+                all = run_join<PACKED>(sm.warp[par][w][lane], all);
+            }
+            if (lane == 0) sm100::mbar_expect_tx(&sm.full[par], K * 512);
+            const uint32_t dst = sm100::saddr(&sm.cta[par][rank][lane]), bar = sm100::saddr(&sm.full[par]);
+            for (int r = 0; r < K; ++r) {
+                uint32_t d, m;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dst), "r"(r));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(bar), "r"(r));
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(d),
+                    "r"(__float_as_uint(all.x)), "r"(__float_as_uint(all.y)), "r"(__float_as_uint(all.z)),
+                    "r"(__float_as_uint(all.w)), "r"(m)
+                    : "memory");
+            }
+            ok = sm100::mbar_wait(&sm.full[par], i >> 1 & 1, &sm.ctl.abort) && ok;
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            float c0 = 0.f, c1 = 0.f;
+            for (int r = 0; r < K; ++r) {
+                if (r == (int)rank) c0 = carry[0], c1 = carry[1];
+                run_through<PACKED>(sm.cta[par][r][lane], carry[0], carry[1]);
+            }
+#pragma unroll
+            for (int w = 0; w < kScanWarps; ++w) {
+                float x0 = c0, x1 = c1;
+                run_through<PACKED>(pre[w], x0, x1);
+                sm.cin[par][w][lane] = make_float2(x0, x1);
+            }
         }
-        return;
+        bar_arrive(kBarCin, kScanPipedThreads);
     }
-    cluster_wait();
-    for (int r = 0; r < K; ++r) {
-        if (r == (int)rank) cin[0] = carry[0], cin[1] = carry[1];
-        run_through<PACKED>(sm.cta[par][r][lane], carry[0], carry[1]);
+    if (!ok && lane == 0 && err) *err = kErrTimeout;
+}
+
+// Before and after the work of a CTA of a cluster: barriers of the exchange ready everywhere,
+// nobody's memory gone while another CTA may still write to it.
+__device__ __forceinline__ void scan_enter(ScanRuns& sm, int K) {
+    if (threadIdx.x == 0) {
+        sm100::mbar_init(&sm.full[0], 1);
+        sm100::mbar_init(&sm.full[1], 1);
+        sm100::mbar_fence_init();
+        sm100::wait_ctl_init(&sm.ctl, 0);
     }
-    run_through<PACKED>(pre, cin[0], cin[1]);
+    __syncthreads();
+    if (K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+__device__ __forceinline__ void scan_leave(int K) {
+    if (K > 1) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Packed input: which of a warp's tokens start or end a sequence.  (lo, hi) is the last
@@ -580,13 +628,13 @@ struct ScanSeq {
     int lo = 0, hi = 0;
     unsigned starts = 0, ends = 0;
     template <int TS, int DIR>
-    __device__ __forceinline__ void find(const ScanParams& p, int64_t t0) {
-        const int64_t a = DIR > 0 ? t0 : t0 - (TS - 1), b = a + TS;    // tokens [a, b)
+    __device__ __forceinline__ void find(const ScanParams& p, int t0) {
+        const int a = DIR > 0 ? t0 : t0 - (TS - 1), b = a + TS;    // tokens [a, b)
         starts = ends = 0;
         if (a > lo && b < hi) return;
         const int lane = threadIdx.x & 31;
-        const int64_t tl = t0 + DIR * (lane < TS ? lane : TS - 1);
-        const int t = (int)(tl < 0 ? 0 : tl < p.T ? tl : p.T - 1);
+        const int tl = t0 + DIR * (lane < TS ? lane : TS - 1);
+        const int t = tl < 0 ? 0 : tl < p.T ? tl : p.T - 1;
         const int n = scan_owner(p.cu, p.N, t);
         const bool in = lane < TS && tl >= 0 && tl < p.T;
         const int s = p.cu[n], e = p.cu[n + 1];
@@ -607,7 +655,7 @@ struct ScanStage {
 };
 
 template <typename X, typename G, int TS, bool PACKED>
-__global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K, int wide) {
+__global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
     ScanStage<X, G, TS, false>& st = *reinterpret_cast<ScanStage<X, G, TS, false>*>(dyn);
     __shared__ ScanRuns sm;
@@ -616,36 +664,49 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
     const bool live = c < p.D, whole = c0 + 64 <= p.D;
-    const ScanSrc<X, TS, 1> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, c0, p.D, wide & 1);
-    const ScanSrc<G, TS, 1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, c0, p.D, wide & 2);
-    X* y = static_cast<X*>(p.y) + b * p.y_sb + c;
     const int step = K * kScanWarps * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
-    int64_t t0 = ((int64_t)rank * kScanWarps + w) * TS;      // this warp's first token of tile i
-    auto load = [&](int64_t t, int s) {
-        const bool inside = whole && t + TS <= p.T;
+    int t0 = ((int)rank * kScanWarps + w) * TS;              // this warp's first token of tile i
+    ScanSrc<X, TS, 1> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
+    ScanSrc<G, TS, 1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
+    X* y = static_cast<X*>(p.y) + b * p.y_sb + c + t0 * p.y_st;
+    const int64_t y_tile = (int64_t)step * p.y_st;
+    auto load = [&](int t, int s) {
+        const bool inside = whole && (unsigned)t + TS <= (unsigned)p.T;
         xs.copy(&st.x[s][w][0][0], t, p.T, inside);
         gs.copy(&st.g[s][w][0][0], t, p.T, inside);
         cp_async_commit();
     };
+    if (w < kScanWarps)
 #pragma unroll
-    for (int s = 0; s < kScanStages; ++s) load(t0 + (int64_t)s * step, s);
+        for (int s = 0; s < kScanStages; ++s) load(t0 + s * step, s);
     if (PACKED) {
         scan_check_cu(p);
-        scan_empty<2>(p, p.s0, p.s0_sn, c, K, rank);
+        if (w < kScanWarps) scan_empty<2>(p, p.s0, p.s0_sn, c, K, rank);
     }
-    float carry[2] = {0.f, 0.f}, cin[2];
-    if (!PACKED && live && p.s0) {
-        carry[0] = p.s0[b * p.s0_sn + c];
-        carry[1] = p.s0[b * p.s0_sn + c + 1];
+    scan_enter(sm, K);
+    if (w == kScanWarps) {
+        float carry[2] = {0.f, 0.f};
+        if (!PACKED && live && p.s0) {
+            carry[0] = p.s0[b * p.s0_sn + c];
+            carry[1] = p.s0[b * p.s0_sn + c + 1];
+        }
+        scan_join<PACKED>(sm, tiles, K, rank, carry, p.err);
+        if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
+            p.fin[b * p.fin_sn + c] = carry[0];
+            p.fin[b * p.fin_sn + c + 1] = carry[1];
+        }
+        scan_leave(K);
+        return;
     }
-    auto initial = [&](int64_t t, float* s) {      // the start state of the sequence that t starts
-        const int n = scan_owner(p.cu, p.N, (int)t);
+    float cin[2];
+    auto initial = [&](int t, float* s) {      // the start state of the sequence that t starts
+        const int n = scan_owner(p.cu, p.N, t);
         s[0] = live && p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
         s[1] = live && p.s0 ? p.s0[n * p.s0_sn + c + 1] : 0.f;
     };
     // the run of this warp's tokens of one tile
-    auto form = [&](int64_t t, int s, unsigned starts) {
+    auto form = [&](int t, int s, unsigned starts) {
         float h[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
@@ -667,9 +728,9 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K
                                 : make_float4(run_decay(L[0]), run_decay(L[1]), h[0], h[1]);
     };
     // the same tokens again from what comes in, to the output
-    auto finish = [&](int64_t t, int s, unsigned starts, unsigned ends) {
-        const int left = (int)min((int64_t)TS, p.T - t);
-        X* o = y + t * p.y_st;
+    auto finish = [&](int t, int s, unsigned starts, unsigned ends) {
+        const int left = min(TS, p.T - t);
+        X* o = y;
 #pragma unroll
         for (int j = 0; j < TS; ++j, o += p.y_st) {
             float xv[2], a[2];
@@ -684,33 +745,27 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K
             cin[1] = fmaf(a[1], cin[1], xv[1]);
             if (live && j < left) st_vec<X, 2>(o, cin);
             if (PACKED && (ends >> j & 1) && live && p.fin) {
-                float* f = p.fin + scan_owner(p.cu, p.N, (int)(t + j)) * p.fin_sn + c;
+                float* f = p.fin + scan_owner(p.cu, p.N, t + j) * p.fin_sn + c;
                 f[0] = cin[0];
                 f[1] = cin[1];
             }
         }
         // the places past the last token hold a = 1, x = 0: they leave h as it is
-        if (!PACKED && left > 0 && t + TS >= p.T && live && p.fin) {
+        if (!PACKED && left > 0 && left >= p.T - t && live && p.fin) {
             p.fin[b * p.fin_sn + c] = cin[0];
             p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
-    if (K > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
     ScanSeq seq;
-    float4 pre = make_float4(1.f, 1.f, 0.f, 0.f);
-    auto next = [&](int64_t t, int s, int par) {   // forms and sends the run of a tile that has landed
+    auto next = [&](int t, int s, int par) {       // the run of a tile that has landed
         __syncwarp();
-        float4 run;
         if (PACKED) {
             seq.find<TS, 1>(p, t);
-            run = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
+            sm.warp[par][w][lane] = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
         } else {
-            run = form(t, s, 0u);
+            sm.warp[par][w][lane] = form(t, s, 0u);
         }
-        runs_send<PACKED>(sm, par, K, rank, run, pre);
+        bar_arrive(kBarRuns, kScanPipedThreads);
     };
     static_assert(kScanStages == 3, "the waits count the tiles behind the one wanted");
     if (tiles > 0) {
@@ -718,8 +773,11 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K
         next(t0, 0, 0);
     }
     int s = 0;
-    for (int i = 0; i < tiles; ++i, t0 += step) {
-        runs_receive<PACKED>(sm, i & 1, K, rank, pre, carry, cin);
+    for (int i = 0; i < tiles; ++i, t0 += step, y += y_tile) {
+        bar_sync(kBarCin, kScanPipedThreads);
+        const float2 in = sm.cin[i & 1][w][lane];
+        cin[0] = in.x;
+        cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
         const int s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
@@ -729,18 +787,15 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_piped(ScanParams p, int K
         if (PACKED && (starts | ends)) finish(t0, s, starts, ends);
         else finish(t0, s, 0u, 0u);
         __syncwarp();
-        load(t0 + (int64_t)kScanStages * step, s);
+        load(t0 + kScanStages * step, s);
         s = s1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!PACKED && p.T == 0 && p.fin && live && rank == 0 && w == 0) {
-        p.fin[b * p.fin_sn + c] = carry[0];
-        p.fin[b * p.fin_sn + c + 1] = carry[1];
-    }
+    scan_leave(K);
 }
 
 template <typename X, typename G, int TS, bool PACKED>
-__global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, int K, int wide) {
+__global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
     ScanStage<X, G, TS, true>& st = *reinterpret_cast<ScanStage<X, G, TS, true>*>(dyn);
     __shared__ ScanRuns sm;
@@ -749,40 +804,53 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, i
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
     const bool live = c < p.D, whole = c0 + 64 <= p.D;
-    const ScanSrc<X, TS, -1> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, c0, p.D, wide & 1);
-    const ScanSrc<G, TS, -1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, c0, p.D, wide & 2);
-    const ScanSrc<X, TS, -1> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, c0, p.D, wide & 4);
-    X* dx = static_cast<X*>(p.y) + b * p.y_sb + c;
-    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c;
     const int step = K * kScanWarps * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
-    int64_t t0 = p.T - 1 - ((int64_t)rank * kScanWarps + w) * TS;    // token of place j of tile i: t0 - j
-    auto load = [&](int64_t t, int s) {
+    int t0 = p.T - 1 - ((int)rank * kScanWarps + w) * TS;    // token of place j of tile i: t0 - j
+    ScanSrc<X, TS, -1> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
+    ScanSrc<G, TS, -1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
+    ScanSrc<X, TS, -1> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, t0 - 1, step, c0, p.D, wide & 4);
+    X* dx = static_cast<X*>(p.y) + b * p.y_sb + c + t0 * p.y_st;
+    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c + t0 * p.dg_st;
+    const int64_t dx_tile = (int64_t)step * p.y_st, dg_tile = (int64_t)step * p.dg_st;
+    auto load = [&](int t, int s) {
         const bool inside = whole && t >= TS - 1;
         ds.copy(&st.x[s][w][0][0], t, p.T, inside);
         gs.copy(&st.g[s][w][0][0], t, p.T, inside);
     };
-    auto load_h = [&](int64_t t, int i) { hs.copy(&st.h[i & 1][w][0][0], t - 1, p.T, whole && t >= TS); };
+    auto load_h = [&](int t, int i) { hs.copy(&st.h[i & 1][w][0][0], t - 1, p.T, whole && t >= TS); };
+    if (w < kScanWarps)
 #pragma unroll
-    for (int s = 0; s < kScanStages; ++s) {
-        load(t0 - (int64_t)s * step, s);
-        if (s < 2) load_h(t0 - (int64_t)s * step, s);
-        cp_async_commit();
-    }
+        for (int s = 0; s < kScanStages; ++s) {
+            load(t0 - s * step, s);
+            if (s < 2) load_h(t0 - s * step, s);
+            cp_async_commit();
+        }
     if (PACKED) {
         scan_check_cu(p);
-        scan_empty<2>(p, p.sT, p.sT_sn, c, K, rank);
+        if (w < kScanWarps) scan_empty<2>(p, p.sT, p.sT_sn, c, K, rank);
     }
-    float carry[2] = {0.f, 0.f}, cin[2];
-    if (!PACKED && live && p.sT) {
-        carry[0] = p.sT[b * p.sT_sn + c];
-        carry[1] = p.sT[b * p.sT_sn + c + 1];
+    scan_enter(sm, K);
+    if (w == kScanWarps) {
+        float carry[2] = {0.f, 0.f};
+        if (!PACKED && live && p.sT) {
+            carry[0] = p.sT[b * p.sT_sn + c];
+            carry[1] = p.sT[b * p.sT_sn + c + 1];
+        }
+        scan_join<PACKED>(sm, tiles, K, rank, carry, p.err);
+        if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
+            p.fin[b * p.fin_sn + c] = carry[0];
+            p.fin[b * p.fin_sn + c + 1] = carry[1];
+        }
+        scan_leave(K);
+        return;
     }
+    float cin[2];
     auto state = [&](const float* src, int64_t sn, int n, float* s) {
         s[0] = live && src ? src[n * sn + c] : 0.f;
         s[1] = live && src ? src[n * sn + c + 1] : 0.f;
     };
-    auto form = [&](int64_t t, int s, unsigned ends) {
+    auto form = [&](int t, int s, unsigned ends) {
         float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
@@ -796,19 +864,19 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, i
                 a[v] = scan_pow2(l);
             }
             if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
-            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, scan_owner(p.cu, p.N, (int)(t - j)), e);
+            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, scan_owner(p.cu, p.N, t - j), e);
             e[0] = a[0] * (dv[0] + e[0]);
             e[1] = a[1] * (dv[1] + e[1]);
         }
         return PACKED && ends ? make_float4(-1.f, -1.f, e[0], e[1])
                               : make_float4(run_decay(L[0]), run_decay(L[1]), e[0], e[1]);
     };
-    auto finish = [&](int64_t t, int s, int hslot, unsigned starts, unsigned ends) {
+    auto finish = [&](int t, int s, int hslot, unsigned starts, unsigned ends) {
         // places up to `left` hold tokens; dense: place left - 1 of the last tile is token 0
-        const int left = (int)max((int64_t)0, min((int64_t)TS, t + 1));
+        const int left = max(0, min(TS, t + 1));
         const bool at0 = !PACKED && left > 0 && t < TS;
-        X* ox = dx + t * p.y_st;
-        G* og = dg + t * p.dg_st;
+        X* ox = dx;
+        G* og = dg;
 #pragma unroll
         for (int j = 0; j < TS; ++j, ox -= p.y_st, og -= p.dg_st) {
             float dv[2], a[2], hv[2];
@@ -820,7 +888,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, i
                 a[1] = scan_pow2(scan_log2(a[1]));
             }
             int n = b;
-            if (PACKED && ((starts | ends) >> j & 1)) n = scan_owner(p.cu, p.N, (int)(t - j));
+            if (PACKED && ((starts | ends) >> j & 1)) n = scan_owner(p.cu, p.N, t - j);
             if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, n, cin);
             if (PACKED ? (starts >> j & 1) : at0 && j == left - 1) state(p.s0, p.s0_sn, n, hv);
             const float d[2] = {dv[0] + cin[0], dv[1] + cin[1]};
@@ -842,30 +910,27 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, i
             p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
-    if (K > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
     ScanSeq seq;
-    float4 pre = make_float4(1.f, 1.f, 0.f, 0.f);
-    auto next = [&](int64_t t, int s, int par) {
+    auto next = [&](int t, int s, int par) {
         __syncwarp();
-        float4 run;
         if (PACKED) {
             seq.find<TS, -1>(p, t);
-            run = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
+            sm.warp[par][w][lane] = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
         } else {
-            run = form(t, s, 0u);
+            sm.warp[par][w][lane] = form(t, s, 0u);
         }
-        runs_send<PACKED>(sm, par, K, rank, run, pre);
+        bar_arrive(kBarRuns, kScanPipedThreads);
     };
     if (tiles > 0) {
         asm volatile("cp.async.wait_group 2;" ::: "memory");
         next(t0, 0, 0);
     }
     int s = 0;
-    for (int i = 0; i < tiles; ++i, t0 -= step) {
-        runs_receive<PACKED>(sm, i & 1, K, rank, pre, carry, cin);
+    for (int i = 0; i < tiles; ++i, t0 -= step, dx -= dx_tile, dg -= dg_tile) {
+        bar_sync(kBarCin, kScanPipedThreads);
+        const float2 in = sm.cin[i & 1][w][lane];
+        cin[0] = in.x;
+        cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
         const int s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
@@ -875,16 +940,13 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_piped(ScanParams p, i
         if (PACKED && (starts | ends)) finish(t0, s, i & 1, starts, ends);
         else finish(t0, s, i & 1, 0u, 0u);
         __syncwarp();
-        load(t0 - (int64_t)kScanStages * step, s);
-        load_h(t0 - 2 * (int64_t)step, i);
+        load(t0 - kScanStages * step, s);
+        load_h(t0 - 2 * step, i);
         cp_async_commit();
         s = s1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!PACKED && p.T == 0 && p.fin && live && rank == 0 && w == 0) {
-        p.fin[b * p.fin_sn + c] = carry[0];
-        p.fin[b * p.fin_sn + c + 1] = carry[1];
-    }
+    scan_leave(K);
 }
 
 struct ScanStepParams {
