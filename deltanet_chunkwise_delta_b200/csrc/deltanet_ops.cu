@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 #include <initializer_list>
 
 #include "../../include/deltanet.h"
@@ -184,11 +183,12 @@ bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
            ok(p.y, p.y_sb, p.y_st, x) && (!bwd || (ok(p.h, p.h_sb, p.h_st, x) && ok(p.dg, p.dg_sb, p.dg_st, g)));
 }
 
-// CTAs per cluster: enough for two on every SM, while each has tokens.
+// CTAs per cluster: about one and a half CTAs on every SM, while each has tokens.  A cluster
+// costs a start and an exchange per tile, idle SMs cost more: 64 channel tiles of 8192 tokens
+// take 108, 72, 61 and 67 us with 1, 2, 4 and 8; 256 of 2048 tokens 52, 60, 68 and 90 us.
 int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
-    if (const char* e = getenv("DN_SCAN_K")) return atoi(e);
     int K = 1;
-    while (K < 8 && items * K < 2 * sms && (int64_t)K * tokens < T) K *= 2;
+    while (K < kScanMaxCluster && items * K < sms + sms / 2 && (int64_t)K * tokens < T) K *= 2;
     return K;
 }
 
@@ -228,14 +228,15 @@ template <typename X, typename G, int V, bool PACKED, bool BWD>
 dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 32 * V - 1) / (32 * V));
     if constexpr (V == 2) {
-        // fp32 rows: half the tokens, for the same bytes on their way
-        constexpr int TS = sizeof(X) == 4 ? 4 : 8;
+        // tokens of a warp's run: as many as leave room for two CTAs on an SM
+        constexpr int TS = sizeof(X) == 4 ? 4 : sizeof(G) == 2 && !BWD ? 16 : 8;
         constexpr int smem = (int)sizeof(ScanStage<X, G, TS, BWD>);
         const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
         const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
         if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-        if constexpr (BWD) return scan_launch(k_scan_bwd_piped<X, G, TS, PACKED>, items, K, kScanPipedThreads, smem, stream, p, wide);
-        else return scan_launch(k_scan_piped<X, G, TS, PACKED>, items, K, kScanPipedThreads, smem, stream, p, wide);
+        auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stream, p, wide); };
+        if constexpr (BWD) return K > 1 ? go(k_scan_bwd_piped<X, G, TS, PACKED, true>) : go(k_scan_bwd_piped<X, G, TS, PACKED, false>);
+        else return K > 1 ? go(k_scan_piped<X, G, TS, PACKED, true>) : go(k_scan_piped<X, G, TS, PACKED, false>);
     } else {
         const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
         if (items > kMax31 / K) return DN_ERR_INVALID_ARG;

@@ -510,21 +510,45 @@ struct ScanSrc {
     }
 };
 
+// Two channels in one instruction.
+__device__ __forceinline__ void fma2(const float* a, const float* b, const float* c, float* d) {
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+        "  fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void add2(const float* a, const float* b, float* d) {
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+        "  add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+__device__ __forceinline__ void mul2(const float* a, const float* b, float* d) {
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+        "  mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+
 // e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
 // relative in all, where a token's step needs no more: a decay's error enters h with weight a.
-__device__ __forceinline__ float scan_log2(float g) { return g * 1.44269504f; }
+__device__ __forceinline__ void scan_log2(float* g) {
+    const float c[2] = {1.44269504f, 1.44269504f};
+    mul2(g, c, g);
+}
 __device__ __forceinline__ float scan_pow2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
+// A warp's run of tile i + 1 is written after it has read what comes into that of tile i: one
+// place.  The other CTAs may be a tile ahead: theirs go by tile parity.
 struct ScanRuns {
-    float4 warp[2][kScanWarps][32];       // (A0, A1, H0, H1) of each warp's run, by tile parity
+    float4 warp[kScanWarps][32];          // (A0, A1, H0, H1) of each warp's run; then, in its
+                                          // first half, what comes into the run
     float4 cta[2][kScanMaxCluster][32];   // of each CTA's run
-    float2 cin[2][kScanWarps][32];        // what comes into each warp's run
     uint64_t full[2];                     // the cluster's runs of a tile have arrived
-    sm100::WaitCtl ctl;
 };
 
 // The product of a run's decays from the sum of their logarithms (base 2), kept below infinity.
@@ -546,27 +570,47 @@ __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync
 __device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 constexpr int kBarRuns = 1, kBarCin = 2;   // named barriers: runs of a tile formed, h before them known
 
+// Waits for a phase that other CTAs of the cluster complete and acquires what they sent (a
+// fence in its place would also wait for this warp's own sends to land: 0.6 us a tile).  Gives
+// up after 2 s.
+__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(sm100::saddr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (i == 255) t0 = sm100::globaltimer();
+        if (i > 255 && sm100::globaltimer() - t0 > sm100::kDefaultWaitNs) return false;
+    }
+}
+
 // The ninth warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
 // into the first tile, in the end what leaves the last one.
-template <bool PACKED>
+template <bool PACKED, bool CL>
 __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsigned rank, float* carry, int* err) {
     const int lane = threadIdx.x & 31;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
         const int par = i & 1;
         bar_sync(kBarRuns, kScanPipedThreads);
-        if (K == 1) {
+        if constexpr (!CL) {
 #pragma unroll
             for (int w = 0; w < kScanWarps; ++w) {
-                sm.cin[par][w][lane] = make_float2(carry[0], carry[1]);
-                run_through<PACKED>(sm.warp[par][w][lane], carry[0], carry[1]);
+                const float4 run = sm.warp[w][lane];
+                *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(carry[0], carry[1]);
+                run_through<PACKED>(run, carry[0], carry[1]);
             }
         } else {
             float4 pre[kScanWarps], all = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kScanWarps; ++w) {
                 pre[w] = all;
-                all = run_join<PACKED>(sm.warp[par][w][lane], all);
+                all = run_join<PACKED>(sm.warp[w][lane], all);
             }
             if (lane == 0) sm100::mbar_expect_tx(&sm.full[par], K * 512);
             const uint32_t dst = sm100::saddr(&sm.cta[par][rank][lane]), bar = sm100::saddr(&sm.full[par]);
@@ -580,8 +624,7 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsign
                     "r"(__float_as_uint(all.w)), "r"(m)
                     : "memory");
             }
-            ok = sm100::mbar_wait(&sm.full[par], i >> 1 & 1, &sm.ctl.abort) && ok;
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            ok = ok && cluster_mbar_wait(&sm.full[par], i >> 1 & 1);
             float c0 = 0.f, c1 = 0.f;
             for (int r = 0; r < K; ++r) {
                 if (r == (int)rank) c0 = carry[0], c1 = carry[1];
@@ -591,7 +634,7 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsign
             for (int w = 0; w < kScanWarps; ++w) {
                 float x0 = c0, x1 = c1;
                 run_through<PACKED>(pre[w], x0, x1);
-                sm.cin[par][w][lane] = make_float2(x0, x1);
+                *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
             }
         }
         bar_arrive(kBarCin, kScanPipedThreads);
@@ -601,21 +644,22 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsign
 
 // Before and after the work of a CTA of a cluster: barriers of the exchange ready everywhere,
 // nobody's memory gone while another CTA may still write to it.
-__device__ __forceinline__ void scan_enter(ScanRuns& sm, int K) {
-    if (threadIdx.x == 0) {
+template <bool CL>
+__device__ __forceinline__ void scan_enter(ScanRuns& sm) {
+    if (CL && threadIdx.x == 0) {
         sm100::mbar_init(&sm.full[0], 1);
         sm100::mbar_init(&sm.full[1], 1);
         sm100::mbar_fence_init();
-        sm100::wait_ctl_init(&sm.ctl, 0);
     }
     __syncthreads();
-    if (K > 1) {
+    if (CL) {
         cluster_arrive();
         cluster_wait();
     }
 }
-__device__ __forceinline__ void scan_leave(int K) {
-    if (K > 1) {
+template <bool CL>
+__device__ __forceinline__ void scan_leave() {
+    if (CL) {
         __syncwarp();
         cluster_arrive();
         cluster_wait();
@@ -645,6 +689,9 @@ struct ScanSeq {
     }
 };
 
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // The tokens on their way, a warp's rows together.  h is read only when a tile is finished,
 // one tile later than x and g: two stages of it are enough.
 template <typename X, typename G, int TS, bool BWD>
@@ -654,12 +701,13 @@ struct ScanStage {
     X h[BWD ? 2 : 1][BWD ? kScanWarps : 1][BWD ? TS : 1][64];
 };
 
-template <typename X, typename G, int TS, bool PACKED>
+template <typename X, typename G, int TS, bool PACKED, bool CL>
 __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
     ScanStage<X, G, TS, false>& st = *reinterpret_cast<ScanStage<X, G, TS, false>*>(dyn);
     __shared__ ScanRuns sm;
-    const unsigned rank = K > 1 ? cluster_rank() : 0;
+    if (!CL) K = 1;
+    const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
@@ -684,19 +732,19 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         scan_check_cu(p);
         if (w < kScanWarps) scan_empty<2>(p, p.s0, p.s0_sn, c, K, rank);
     }
-    scan_enter(sm, K);
+    scan_enter<CL>(sm);
     if (w == kScanWarps) {
         float carry[2] = {0.f, 0.f};
         if (!PACKED && live && p.s0) {
             carry[0] = p.s0[b * p.s0_sn + c];
             carry[1] = p.s0[b * p.s0_sn + c + 1];
         }
-        scan_join<PACKED>(sm, tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL>(sm, tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
-        scan_leave(K);
+        scan_leave<CL>();
         return;
     }
     float cin[2];
@@ -713,16 +761,13 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
             float xv[2], a[2];
             unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
             unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float l = scan_log2(a[v]);
-                L[v] += l;
-                a[v] = scan_pow2(l);
-            }
+            scan_log2(a);
+            add2(L, a, L);
+            a[0] = scan_pow2(a[0]);
+            a[1] = scan_pow2(a[1]);
             if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
             if (PACKED && (starts >> j & 1)) initial(t + j, h);
-            h[0] = fmaf(a[0], h[0], xv[0]);
-            h[1] = fmaf(a[1], h[1], xv[1]);
+            fma2(a, h, xv, h);
         }
         return PACKED && starts ? make_float4(-1.f, -1.f, h[0], h[1])
                                 : make_float4(run_decay(L[0]), run_decay(L[1]), h[0], h[1]);
@@ -737,12 +782,12 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
             unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
             unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
             if constexpr (sizeof(G) == 2) {
-                a[0] = scan_pow2(scan_log2(a[0]));
-                a[1] = scan_pow2(scan_log2(a[1]));
+                scan_log2(a);
+                a[0] = scan_pow2(a[0]);
+                a[1] = scan_pow2(a[1]);
             }
             if (PACKED && (starts >> j & 1)) initial(t + j, cin);
-            cin[0] = fmaf(a[0], cin[0], xv[0]);
-            cin[1] = fmaf(a[1], cin[1], xv[1]);
+            fma2(a, cin, xv, cin);
             if (live && j < left) st_vec<X, 2>(o, cin);
             if (PACKED && (ends >> j & 1) && live && p.fin) {
                 float* f = p.fin + scan_owner(p.cu, p.N, t + j) * p.fin_sn + c;
@@ -757,32 +802,32 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         }
     };
     ScanSeq seq;
-    auto next = [&](int t, int s, int par) {       // the run of a tile that has landed
+    auto next = [&](int t, int s) {       // the run of a tile that has landed
         __syncwarp();
         if (PACKED) {
             seq.find<TS, 1>(p, t);
-            sm.warp[par][w][lane] = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
+            sm.warp[w][lane] = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
         } else {
-            sm.warp[par][w][lane] = form(t, s, 0u);
+            sm.warp[w][lane] = form(t, s, 0u);
         }
         bar_arrive(kBarRuns, kScanPipedThreads);
     };
     static_assert(kScanStages == 3, "the waits count the tiles behind the one wanted");
     if (tiles > 0) {
         asm volatile("cp.async.wait_group 2;" ::: "memory");
-        next(t0, 0, 0);
+        next(t0, 0);
     }
     int s = 0;
     for (int i = 0; i < tiles; ++i, t0 += step, y += y_tile) {
         bar_sync(kBarCin, kScanPipedThreads);
-        const float2 in = sm.cin[i & 1][w][lane];
+        const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
         cin[0] = in.x;
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
         const int s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            next(t0 + step, s1, (i + 1) & 1);
+            next(t0 + step, s1);
         }
         if (PACKED && (starts | ends)) finish(t0, s, starts, ends);
         else finish(t0, s, 0u, 0u);
@@ -791,15 +836,16 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         s = s1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    scan_leave(K);
+    scan_leave<CL>();
 }
 
-template <typename X, typename G, int TS, bool PACKED>
+template <typename X, typename G, int TS, bool PACKED, bool CL>
 __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
     ScanStage<X, G, TS, true>& st = *reinterpret_cast<ScanStage<X, G, TS, true>*>(dyn);
     __shared__ ScanRuns sm;
-    const unsigned rank = K > 1 ? cluster_rank() : 0;
+    if (!CL) K = 1;
+    const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
@@ -830,19 +876,19 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         scan_check_cu(p);
         if (w < kScanWarps) scan_empty<2>(p, p.sT, p.sT_sn, c, K, rank);
     }
-    scan_enter(sm, K);
+    scan_enter<CL>(sm);
     if (w == kScanWarps) {
         float carry[2] = {0.f, 0.f};
         if (!PACKED && live && p.sT) {
             carry[0] = p.sT[b * p.sT_sn + c];
             carry[1] = p.sT[b * p.sT_sn + c + 1];
         }
-        scan_join<PACKED>(sm, tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL>(sm, tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
-        scan_leave(K);
+        scan_leave<CL>();
         return;
     }
     float cin[2];
@@ -857,16 +903,14 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
             float dv[2], a[2];
             unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), dv);
             unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float l = scan_log2(a[v]);
-                L[v] += l;
-                a[v] = scan_pow2(l);
-            }
+            scan_log2(a);
+            add2(L, a, L);
+            a[0] = scan_pow2(a[0]);
+            a[1] = scan_pow2(a[1]);
             if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
             if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, scan_owner(p.cu, p.N, t - j), e);
-            e[0] = a[0] * (dv[0] + e[0]);
-            e[1] = a[1] * (dv[1] + e[1]);
+            add2(dv, e, e);
+            mul2(a, e, e);
         }
         return PACKED && ends ? make_float4(-1.f, -1.f, e[0], e[1])
                               : make_float4(run_decay(L[0]), run_decay(L[1]), e[0], e[1]);
@@ -884,18 +928,19 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
             unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
             unpack(ld_raw<X, 2>(&st.h[hslot][w][j][lane * 2]), hv);
             if constexpr (sizeof(G) == 2) {
-                a[0] = scan_pow2(scan_log2(a[0]));
-                a[1] = scan_pow2(scan_log2(a[1]));
+                scan_log2(a);
+                a[0] = scan_pow2(a[0]);
+                a[1] = scan_pow2(a[1]);
             }
             int n = b;
             if (PACKED && ((starts | ends) >> j & 1)) n = scan_owner(p.cu, p.N, t - j);
             if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, n, cin);
             if (PACKED ? (starts >> j & 1) : at0 && j == left - 1) state(p.s0, p.s0_sn, n, hv);
-            const float d[2] = {dv[0] + cin[0], dv[1] + cin[1]};
-            cin[0] = a[0] * d[0];
-            cin[1] = a[1] * d[1];
+            float d[2], q[2];
+            add2(dv, cin, d);
+            mul2(a, d, cin);
+            mul2(cin, hv, q);
             if (live && j < left) {
-                const float q[2] = {cin[0] * hv[0], cin[1] * hv[1]};
                 st_vec<X, 2>(ox, d);
                 st_vec<G, 2>(og, q);
             }
@@ -911,31 +956,31 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         }
     };
     ScanSeq seq;
-    auto next = [&](int t, int s, int par) {
+    auto next = [&](int t, int s) {
         __syncwarp();
         if (PACKED) {
             seq.find<TS, -1>(p, t);
-            sm.warp[par][w][lane] = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
+            sm.warp[w][lane] = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
         } else {
-            sm.warp[par][w][lane] = form(t, s, 0u);
+            sm.warp[w][lane] = form(t, s, 0u);
         }
         bar_arrive(kBarRuns, kScanPipedThreads);
     };
     if (tiles > 0) {
         asm volatile("cp.async.wait_group 2;" ::: "memory");
-        next(t0, 0, 0);
+        next(t0, 0);
     }
     int s = 0;
     for (int i = 0; i < tiles; ++i, t0 -= step, dx -= dx_tile, dg -= dg_tile) {
         bar_sync(kBarCin, kScanPipedThreads);
-        const float2 in = sm.cin[i & 1][w][lane];
+        const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
         cin[0] = in.x;
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
         const int s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            next(t0 - step, s1, (i + 1) & 1);
+            next(t0 - step, s1);
         }
         if (PACKED && (starts | ends)) finish(t0, s, i & 1, starts, ends);
         else finish(t0, s, i & 1, 0u, 0u);
@@ -946,7 +991,7 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         s = s1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    scan_leave(K);
+    scan_leave<CL>();
 }
 
 struct ScanStepParams {
