@@ -1,9 +1,8 @@
 """Builds the sm_100a shared library behind the C ABI (include/deltanet.h).
 
-``python -m deltanet_chunkwise_delta_b200.build`` compiles ``csrc/deltanet.cu``,
-``csrc/deltanet_noalloc.cu`` and ``csrc/deltanet_ops.cu`` with nvcc into
-``_build/libdeltanet_b200.so`` inside the package directory, so the library travels
-with the source tree.
+``python -m deltanet_chunkwise_delta_b200.build`` compiles the ``csrc/*.cu``
+files with nvcc into ``_build/libdeltanet_b200.so`` inside the package directory, so
+the library travels with the source tree.
 """
 from __future__ import annotations
 
@@ -15,7 +14,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name)
-        for name in ("deltanet.cu", "deltanet_noalloc.cu", "deltanet_ops.cu")]
+        for name in ("deltanet.cu", "deltanet_noalloc.cu", "deltanet_ops.cu", "deltanet_norm.cu")]
 LIB = os.path.join(PKG, "_build", "libdeltanet_b200.so")
 
 NVCC_FLAGS = [

@@ -1,16 +1,13 @@
 // Host side of the operators around the delta-rule kernels (include/deltanet.h):
-// deltanet_step, deltanet_scan_* and deltanet_norm_*.  Argument checks and launches only.
+// deltanet_step and deltanet_scan_*.  Argument checks and launches only.
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <initializer_list>
 
 #include "../../include/deltanet.h"
 #include "dn_host.h"
-#include "dn_norm.cuh"
 #include "dn_scan.cuh"
 #include "dn_step.cuh"
 
@@ -18,93 +15,12 @@ using namespace dn;
 
 namespace {
 
-constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
-
-// A tensor of the given shape: a dtype of the mask, last stride 1, non-negative strides,
-// data aligned to its element (any address where it has no elements).
-constexpr int kF32 = 1 << DN_F32, kBf16 = 1 << DN_BF16;
-bool view_ok(const dn_tensor* t, int ndim, const int64_t* dims, int dtypes) {
-    if (!shape_eq(t, ndim, dims) || t->dtype < 0 || t->dtype > 2 || !(dtypes >> t->dtype & 1)) return false;
-    for (int i = 0; i < ndim; ++i)
-        if (t->stride[i] < 0) return false;
-    if (t->shape[ndim - 1] > 1 && t->stride[ndim - 1] != 1) return false;
-    if (numel(t) == 0) return true;
-    return t->data && reinterpret_cast<uintptr_t>(t->data) % elem_size(t->dtype) == 0;
-}
-
-// No two elements of an output share an address.
-bool distinct(const dn_tensor* t) {
-    if (numel(t) == 0) return true;
-    int order[4];
-    for (int i = 0; i < t->ndim; ++i) order[i] = i;
-    std::sort(order, order + t->ndim, [&](int a, int b) { return t->stride[a] < t->stride[b]; });
-    int64_t extent = 1;
-    for (int i = 0; i < t->ndim; ++i) {
-        const int o = order[i];
-        if (t->shape[o] == 1) continue;
-        if (t->stride[o] < extent) return false;
-        extent += t->stride[o] * (t->shape[o] - 1);
-    }
-    return true;
-}
-
-// Rows side by side in one buffer: equal shapes and strides, and the two rows apart within
-// the smallest row pitch, which divides the larger ones.
-bool interleaved(const dn_tensor* a, const dn_tensor* b) {
-    if (a->ndim != b->ndim || a->ndim < 2) return false;
-    const int64_t es = elem_size(a->dtype);
-    if (es != elem_size(b->dtype)) return false;
-    int64_t pitch = 0;
-    for (int i = 0; i < a->ndim; ++i) {
-        if (a->shape[i] != b->shape[i]) return false;
-        if (i == a->ndim - 1 || a->shape[i] == 1) continue;
-        if (a->stride[i] != b->stride[i] || a->stride[i] < 1) return false;
-        pitch = pitch ? std::min(pitch, a->stride[i]) : a->stride[i];
-    }
-    if (!pitch) return false;
-    for (int i = 0; i + 1 < a->ndim; ++i)
-        if (a->shape[i] > 1 && a->stride[i] % pitch) return false;
-    const int64_t S = pitch * es, L = a->shape[a->ndim - 1] * es;
-    int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data)) % S;
-    if (off < 0) off += S;
-    return off >= L && off + L <= S;
-}
-
-bool clash(const dn_tensor* a, const dn_tensor* b) { return overlap(a, b) && !interleaved(a, b); }
-
-// DN_ERR_INVALID_ARG for an output whose own elements overlap, DN_ERR_ALIAS for one that
-// overlaps an input or another output (null entries are skipped).
-dn_status alias_check(std::initializer_list<const dn_tensor*> outs, std::initializer_list<const dn_tensor*> ins) {
-    for (const dn_tensor* o : outs)
-        if (o && !distinct(o)) return DN_ERR_INVALID_ARG;
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
-        for (const dn_tensor* in : ins)
-            if (in && clash(*o, in)) return DN_ERR_ALIAS;
-        for (auto o2 = o + 1; o2 != outs.end(); ++o2)
-            if (*o2 && clash(*o, *o2)) return DN_ERR_ALIAS;
-    }
-    return DN_OK;
-}
-
-bool index_ok(const dn_tensor* t, int64_t min_len) {
-    return t->ndim == 1 && t->dtype == DN_I32 && t->shape[0] >= min_len &&
-           (t->shape[0] <= 1 || t->stride[0] == 1) && (t->shape[0] == 0 || t->data) &&
-           reinterpret_cast<uintptr_t>(t->data) % 4 == 0;
-}
-
 // [B, T, H] fp32 scalars per token and head, any non-negative strides.
 bool scalars_ok(const dn_tensor* t, const int64_t* dims) {
     if (!shape_eq(t, 3, dims) || t->dtype != DN_F32) return false;
     for (int i = 0; i < 3; ++i)
         if (t->stride[i] < 0) return false;
     return numel(t) == 0 || (t->data && reinterpret_cast<uintptr_t>(t->data) % 4 == 0);
-}
-
-dn_status launched(int n) {
-    if (cudaGetLastError() != cudaSuccess) return DN_ERR_CUDA;
-    dn_note_launches(n);
-    return DN_OK;
 }
 
 template <typename E, int DK, int DV>
@@ -274,74 +190,6 @@ void set_state(const dn_tensor* t, P*& ptr, int64_t& stride) {
     }
 }
 
-bool param_ok(const dn_tensor* t, int64_t d, int dtypes) { return view_ok(t, 1, &d, dtypes); }
-
-ParamVec param(const dn_tensor* t) {
-    ParamVec v;
-    v.p = t ? t->data : nullptr;
-    v.bf16 = t && t->dtype == DN_BF16;
-    return v;
-}
-
-RowRef row_ref(const dn_tensor* t) {
-    RowRef r = {nullptr, 0, 0, 0};
-    if (!t) return r;
-    r.p = t->data;
-    r.s0 = t->stride[0];
-    r.s1 = t->ndim > 2 ? t->stride[1] : 0;
-    r.s2 = t->ndim > 3 ? t->stride[2] : 0;
-    return r;
-}
-
-// The arguments that deltanet_norm_fwd and _bwd share.
-dn_status norm_check(const dn_tensor* y, const dn_tensor* w, const dn_tensor* gate, int act, const dn_tensor* res,
-                     const dn_tensor* sc, const dn_tensor* nw, float eps, NormParams& p) {
-    if (!y || y->ndim < 2 || y->ndim > 4) return DN_ERR_INVALID_ARG;
-    if (!w && !gate && !res) return DN_ERR_INVALID_ARG;
-    if ((sc || nw) && !res) return DN_ERR_INVALID_ARG;
-    if (act != DN_ACT_SILU && act != DN_ACT_SIGMOID) return DN_ERR_INVALID_ARG;
-    if (!(eps >= 0.f) || std::isinf(eps)) return DN_ERR_INVALID_ARG;
-    const int64_t d = y->shape[y->ndim - 1];
-    int64_t rows = 1;
-    if (d < 1) return DN_ERR_INVALID_ARG;
-    for (int i = 0; i + 1 < y->ndim; ++i) {
-        if (y->shape[i] < 0 || y->shape[i] > kMax31) return DN_ERR_INVALID_ARG;
-        rows *= y->shape[i];
-        if (rows > kMax31) return DN_ERR_INVALID_ARG;
-    }
-    if (!view_ok(y, y->ndim, y->shape, kF32 | kBf16)) return DN_ERR_INVALID_ARG;
-    const int yt = 1 << y->dtype;
-    if (gate && !view_ok(gate, y->ndim, y->shape, yt)) return DN_ERR_INVALID_ARG;
-    if (res && !view_ok(res, y->ndim, y->shape, yt | kF32)) return DN_ERR_INVALID_ARG;
-    for (const dn_tensor* t : {w, sc, nw})
-        if (t && !param_ok(t, d, kF32 | kBf16)) return DN_ERR_INVALID_ARG;
-    if (d > kNormMaxD) return DN_ERR_UNSUPPORTED;
-    std::memset(&p, 0, sizeof p);
-    p.y = row_ref(y);
-    p.gate = row_ref(gate);
-    p.res = row_ref(res);
-    p.w = param(w);
-    p.sc = param(sc);
-    p.nw = param(nw);
-    p.act = act;
-    p.eps = eps;
-    p.rows = rows;
-    p.d = (int)d;
-    p.n1 = y->ndim > 2 ? (unsigned)y->shape[1] : 1;
-    p.n2 = y->ndim > 3 ? (unsigned)y->shape[2] : 1;
-    return DN_OK;
-}
-
-// Kernel choice by the dtypes of y and the residual: f(Y(), R()).
-template <typename F>
-void by_row_types(const dn_tensor* y, const dn_tensor* res, F f) {
-    if (y->dtype == DN_F32) f(float(), float());
-    else if (res && res->dtype == DN_F32) f(__nv_bfloat16(), float());
-    else f(__nv_bfloat16(), __nv_bfloat16());
-}
-
-int norm_bwd_ctas(int64_t rows) { return (int)std::min<int64_t>(rows, kNormBwdCtas); }
-
 }  // namespace
 
 extern "C" {
@@ -494,100 +342,6 @@ dn_status deltanet_scan_step(const dn_tensor* x, const dn_tensor* g, dn_tensor* 
         k_scan_step<decltype(xt), decltype(gt)><<<grid, kScanThreads, 0, stream>>>(p);
     });
     return launched(1);
-}
-
-dn_status deltanet_norm_fwd(const dn_tensor* y, const dn_tensor* weight, const dn_tensor* gate, int activation,
-                            const dn_tensor* residual, const dn_tensor* scale, const dn_tensor* next_weight,
-                            float eps, dn_tensor* out, dn_tensor* residual_out, void* stream_ptr) {
-    NormParams p;
-    dn_status st = norm_check(y, weight, gate, activation, residual, scale, next_weight, eps, p);
-    if (st != DN_OK) return st;
-    if ((out != nullptr) != (!residual || next_weight) || (residual_out != nullptr) != (residual != nullptr))
-        return DN_ERR_INVALID_ARG;
-    if (out && !view_ok(out, y->ndim, y->shape, 1 << y->dtype)) return DN_ERR_INVALID_ARG;
-    if (residual && !view_ok(residual_out, y->ndim, y->shape, 1 << residual->dtype)) return DN_ERR_INVALID_ARG;
-    if ((st = alias_check({out, residual_out}, {y, weight, gate, residual, scale, next_weight})) != DN_OK) return st;
-    int dev = 0, sms = 0;
-    if ((st = dn_device_check(dev, sms)) != DN_OK) return st;
-    if (p.rows == 0) return DN_OK;
-    p.out = row_ref(out);
-    p.rout = row_ref(residual_out);
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    by_row_types(y, residual, [&](auto yt, auto rt) {
-        k_norm_fwd<decltype(yt), decltype(rt)><<<(unsigned)p.rows, kNormThreads, 0, stream>>>(p);
-    });
-    return launched(1);
-}
-
-int64_t deltanet_norm_workspace(int64_t rows, int64_t d) {
-    return rows > 0 && d > 0 ? (int64_t)norm_bwd_ctas(rows) * 3 * d : 0;
-}
-
-dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const dn_tensor* gate, int activation,
-                            const dn_tensor* residual, const dn_tensor* scale, const dn_tensor* next_weight,
-                            float eps, const dn_tensor* d_out, const dn_tensor* d_residual_out, dn_tensor* d_y,
-                            dn_tensor* d_weight, dn_tensor* d_gate, dn_tensor* d_residual, dn_tensor* d_scale,
-                            dn_tensor* d_next_weight, dn_tensor* workspace, void* stream_ptr) {
-    NormParams p;
-    dn_status st = norm_check(y, weight, gate, activation, residual, scale, next_weight, eps, p);
-    if (st != DN_OK) return st;
-    const int nd = y->ndim, yt = 1 << y->dtype, rt = residual ? 1 << residual->dtype : 0;
-    const int64_t d = p.d;
-    if ((d_out != nullptr) != (!residual || next_weight)) return DN_ERR_INVALID_ARG;
-    if (d_residual_out ? !residual : residual && !next_weight) return DN_ERR_INVALID_ARG;
-    if (d_out && !view_ok(d_out, nd, y->shape, yt)) return DN_ERR_INVALID_ARG;
-    if (d_residual_out && !view_ok(d_residual_out, nd, y->shape, rt)) return DN_ERR_INVALID_ARG;
-    if (!d_y || !view_ok(d_y, nd, y->shape, yt)) return DN_ERR_INVALID_ARG;
-    if ((d_gate != nullptr) != (gate != nullptr) || (d_residual != nullptr) != (residual != nullptr))
-        return DN_ERR_INVALID_ARG;
-    if (d_gate && !view_ok(d_gate, nd, y->shape, yt)) return DN_ERR_INVALID_ARG;
-    if (d_residual && !view_ok(d_residual, nd, y->shape, rt)) return DN_ERR_INVALID_ARG;
-    const dn_tensor* params[3] = {weight, scale, next_weight};
-    const dn_tensor* grads[3] = {d_weight, d_scale, d_next_weight};
-    bool sums = false;
-    for (int i = 0; i < 3; ++i) {
-        if ((params[i] != nullptr) != (grads[i] != nullptr)) return DN_ERR_INVALID_ARG;
-        if (grads[i] && !param_ok(grads[i], d, kF32)) return DN_ERR_INVALID_ARG;
-        sums |= grads[i] != nullptr;
-    }
-    const int64_t need = sums ? deltanet_norm_workspace(p.rows, d) : 0;
-    if (need > 0 && (!workspace || workspace->ndim != 1 || workspace->dtype != DN_F32 || !workspace->data ||
-                     workspace->stride[0] != 1 || !aligned16(workspace->data)))
-        return DN_ERR_INVALID_ARG;
-    if (need > 0 && workspace->shape[0] < need) return DN_ERR_WORKSPACE;
-    if ((st = alias_check({d_y, d_gate, d_residual, d_weight, d_scale, d_next_weight, need > 0 ? workspace : nullptr},
-                          {y, weight, gate, residual, scale, next_weight, d_out, d_residual_out})) != DN_OK)
-        return st;
-    int dev = 0, sms = 0;
-    if ((st = dn_device_check(dev, sms)) != DN_OK) return st;
-    p.dout = row_ref(d_out);
-    p.drout = row_ref(d_residual_out);
-    p.dy = row_ref(d_y);
-    p.dgate = row_ref(d_gate);
-    p.dres = row_ref(d_residual);
-    p.part = need > 0 ? static_cast<float*>(workspace->data) : nullptr;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    const int ctas = norm_bwd_ctas(p.rows);
-    int launches = 0;
-    if (p.rows > 0) {
-        const int smem = (int)(3 * d * sizeof(float));
-        bool ok = true;
-        by_row_types(y, residual, [&](auto yt, auto rt) {
-            auto* kern = k_norm_bwd<decltype(yt), decltype(rt)>;
-            ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kNormMaxD * 4) ==
-                 cudaSuccess;
-            if (ok) kern<<<ctas, kNormThreads, smem, stream>>>(p);
-        });
-        if (!ok) return DN_ERR_CUDA;
-        ++launches;
-    }
-    if (sums) {
-        auto f = [](dn_tensor* t) { return t ? static_cast<float*>(t->data) : nullptr; };
-        k_norm_bwd_sum<<<dim3((unsigned)((d + 31) / 32), 3), 256, 0, stream>>>(
-            p.part, ctas, (int)d, f(d_weight), f(d_scale), f(d_next_weight));
-        ++launches;
-    }
-    return launched(launches);
 }
 
 }  // extern "C"

@@ -18,7 +18,7 @@ namespace dn {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxD = 16384;
-constexpr int kNormBwdCtas = 296;      // most CTAs of the backward kernel (partial sums kept)
+constexpr int kNormBwdCtas = 444;      // most CTAs of the backward kernels (partial sums kept)
 
 // A row tensor: element strides of up to three row dimensions (see NormParams::n1, n2).
 struct RowRef {
@@ -44,9 +44,10 @@ __device__ __forceinline__ E* row_ptr(const RowRef& r, unsigned i0, unsigned i1,
     return static_cast<E*>(const_cast<void*>(r.p)) + i0 * r.s0 + i1 * r.s1 + i2 * r.s2;
 }
 
-// act(z) and act'(z)
+// act(z) and act'(z) from s = 1 / (1 + e^-z): the hardware's 2^x and 1/x, a few ulp each.  Far
+// out e^-z is inf or 0 and s is 0 or 1.
 __device__ __forceinline__ float norm_act(float z, int act, float* grad = nullptr) {
-    const float s = 1.f / (1.f + expf(-z));
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
     if (act == 1) {
         if (grad) *grad = s * (1.f - s);
         return s;
@@ -66,6 +67,408 @@ __device__ __forceinline__ float cta_sum(float x, float* sh) {
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += sh[w];
     return s;
 }
+
+// ---- rows that fit a group of threads, 8 elements each -----------------------------------
+//
+// TPR threads hold a row in registers (8, 16 or 32 of a warp, or a whole CTA): every element is
+// read and written once, the sums over the row go through shuffles and, for a CTA, one barrier
+// each.  CTAs stay and walk the rows; with 16-byte rows (VEC) the next row is on its way
+// (cp.async, each thread its own pieces, no barrier) while one is worked on.  Without, a
+// thread's elements lie TPR apart.
+
+template <int TPR>
+constexpr int kNormCta = TPR <= 32 ? kNormThreads : TPR;
+
+// The sums of N values over the row's threads, on all of them; `turn` alternates between calls.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float* v, float (*sh)[2][32], int& turn) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(~0u, v[n], o);
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) sh[turn][n][threadIdx.x >> 5] = v[n];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = 0.f;
+            if constexpr (W <= 8) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) s += sh[turn][n][w];
+            } else {
+                s = (threadIdx.x & 31) < W ? sh[turn][n][threadIdx.x & 31] : 0.f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+            }
+            v[n] = s;
+        }
+        turn ^= 1;
+    }
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
+// A thread's 8 elements of a row.
+template <typename E, int TPR, bool VEC>
+struct RowPart {
+    static constexpr int kPieces = sizeof(E) / 2;      // of 16 bytes
+    __device__ static __forceinline__ int col(int l, int e) { return VEC ? l * 8 + e : e * TPR + l; }
+    __device__ static __forceinline__ void unpack16(const uint4* q, float* f) {
+        if constexpr (sizeof(E) == 2) {
+            const uint32_t u[4] = {q->x, q->y, q->z, q->w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack(u[i], f + 2 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(q[i].x);
+                f[4 * i + 1] = __uint_as_float(q[i].y);
+                f[4 * i + 2] = __uint_as_float(q[i].z);
+                f[4 * i + 3] = __uint_as_float(q[i].w);
+            }
+        }
+    }
+    __device__ static __forceinline__ void load(const E* row, int l, int d, float* f) {
+        if constexpr (VEC) {
+            uint4 q[kPieces] = {};
+            if (l * 8 < d)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(row + l * 8) + i);
+            unpack16(q, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = col(l, e) < d ? ld_elem(row + col(l, e)) : 0.f;
+        }
+    }
+    __device__ static __forceinline__ void store(E* row, int l, int d, const float* f) {
+        if constexpr (VEC) {
+            if (l * 8 >= d) return;
+            if constexpr (sizeof(E) == 2) {
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pack(f + 2 * i, u[i]);
+                *reinterpret_cast<uint4*>(row + l * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+                float4* o = reinterpret_cast<float4*>(row + l * 8);
+                o[0] = make_float4(f[0], f[1], f[2], f[3]);
+                o[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col(l, e) < d) st_elem(row + col(l, e), f[e]);
+        }
+    }
+    // this thread's pieces into shared memory (16 bytes a thread side by side), and from there
+    __device__ static __forceinline__ void fetch(const E* row, int l, int d, uint4* place) {
+        if (l * 8 < d)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                cp_async16(place + i * kNormCta<TPR>, reinterpret_cast<const uint4*>(row + l * 8) + i);
+    }
+    __device__ static __forceinline__ void take(const uint4* place, int l, int d, float* f) {
+        uint4 q[kPieces] = {};
+        if (l * 8 < d)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) q[i] = place[i * kNormCta<TPR>];
+        unpack16(q, f);
+    }
+};
+
+// 8 of a parameter vector (`none` where it is not given)
+template <int TPR, bool VEC>
+__device__ __forceinline__ void param_part(const ParamVec& v, int l, int d, float none, float* f) {
+    if (!v.p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = none;
+    } else if (VEC && v.vec) {
+        if (v.bf16) RowPart<__nv_bfloat16, TPR, true>::load(static_cast<const __nv_bfloat16*>(v.p), l, d, f);
+        else RowPart<float, TPR, true>::load(static_cast<const float*>(v.p), l, d, f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = RowPart<float, TPR, VEC>::col(l, e);
+            f[e] = c < d ? ld_param(v, c) : 0.f;
+        }
+    }
+}
+
+struct RowAt {
+    unsigned i0, i1, i2;
+    __device__ __forceinline__ RowAt(const NormParams& p, unsigned row) {
+        const unsigned q = p.n2 == 1 ? row : row / p.n2;
+        i2 = row - q * p.n2;
+        i0 = p.n1 == 1 ? q : q / p.n1;
+        i1 = q - i0 * p.n1;
+    }
+    template <typename E>
+    __device__ __forceinline__ E* of(const RowRef& r) const { return row_ptr<E>(r, i0, i1, i2); }
+};
+
+// Rounds of 16 bytes per thread in shared memory: where each operand's begin, and their number.
+template <typename Y, typename R>
+struct NormPlan {
+    int z, dout, r, dr, all;
+    __host__ __device__ NormPlan(const NormParams& p) {
+        constexpr int nY = sizeof(Y) / 2, nR = sizeof(R) / 2;
+        z = nY;
+        dout = z + (p.gate.p ? nY : 0);
+        r = dout + (p.dout.p ? nY : 0);
+        dr = r + (p.res.p ? nR : 0);
+        all = dr + (p.drout.p ? nR : 0);
+    }
+};
+
+template <typename Y, typename R, int TPR, bool VEC, bool RES>
+__global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
+    using PY = RowPart<Y, TPR, VEC>;
+    using PR = RowPart<R, TPR, VEC>;
+    constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
+    extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
+    __shared__ float sh[2][2][32];
+    const NormPlan<Y, R> plan(p);
+    auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
+    const int l = threadIdx.x % TPR, d = p.d;
+    int turn = 0, s = 0;
+    const float inv = 1.f / (float)d;
+    float w[8], sc[8], nw[8];
+    param_part<TPR, VEC>(p.w, l, d, 1.f, w);
+    if (RES) {
+        param_part<TPR, VEC>(p.sc, l, d, 1.f, sc);
+        param_part<TPR, VEC>(p.nw, l, d, 1.f, nw);
+    }
+    auto fetch = [&](int64_t base, int s) {
+        if constexpr (VEC) {
+            const int64_t row = base + threadIdx.x / TPR;
+            if (row < p.rows) {
+                const RowAt at(p, (unsigned)row);
+                PY::fetch(at.of<const Y>(p.y), l, d, place(s, 0));
+                if (p.gate.p) PY::fetch(at.of<const Y>(p.gate), l, d, place(s, plan.z));
+                if (RES) PR::fetch(at.of<const R>(p.res), l, d, place(s, plan.r));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t base = (int64_t)blockIdx.x * ROWS;
+    fetch(base, 0);
+    for (; base < p.rows; base += step, s ^= 1) {
+        fetch(base + step, s ^ 1);
+        if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int64_t row = base + threadIdx.x / TPR;
+        const bool on = row < p.rows;
+        const int dd = on ? d : 0;                     // rows past the last: no elements
+        const RowAt at(p, on ? (unsigned)row : 0u);
+        float v[8], z[8], r[8];
+        if constexpr (VEC) {
+            PY::take(place(s, 0), l, dd, v);
+            if (p.gate.p) PY::take(place(s, plan.z), l, dd, z);
+            if (RES) PR::take(place(s, plan.r), l, dd, r);
+        } else {
+            PY::load(at.of<const Y>(p.y), l, dd, v);
+            if (p.gate.p) PY::load(at.of<const Y>(p.gate), l, dd, z);
+            if (RES) PR::load(at.of<const R>(p.res), l, dd, r);
+        }
+        if (p.w.p) {
+            float q = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+            row_sum<TPR, 1>(&q, sh, turn);
+            const float rstd = rsqrtf(q * inv + p.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= rstd * w[e];
+        }
+        if (p.gate.p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= norm_act(z[e], p.act);
+        if constexpr (!RES) {
+            if (on) PY::store(at.of<Y>(p.out), l, d, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(sc[e], v[e], r[e]);
+            if (on) PR::store(at.of<R>(p.rout), l, d, v);
+            if (p.nw.p) {
+                float q = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+                row_sum<TPR, 1>(&q, sh, turn);
+                const float rstd = rsqrtf(q * inv + p.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= rstd * nw[e];
+                if (on) PY::store(at.of<Y>(p.out), l, d, v);
+            }
+        }
+    }
+    if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename Y, typename R, int TPR, bool VEC, bool RES>
+__global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
+    using PY = RowPart<Y, TPR, VEC>;
+    using PR = RowPart<R, TPR, VEC>;
+    constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
+    extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
+    __shared__ float sh[2][2][32];
+    const NormPlan<Y, R> plan(p);
+    auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
+    const int l = threadIdx.x % TPR, d = p.d;
+    int turn = 0, s = 0;
+    const float inv = 1.f / (float)d;
+    float aw[8] = {}, as[8] = {}, an[8] = {};          // sums over this thread's rows
+    auto fetch = [&](int64_t base, int s) {
+        if constexpr (VEC) {
+            const int64_t row = base + threadIdx.x / TPR;
+            if (row < p.rows) {
+                const RowAt at(p, (unsigned)row);
+                PY::fetch(at.of<const Y>(p.y), l, d, place(s, 0));
+                if (p.gate.p) PY::fetch(at.of<const Y>(p.gate), l, d, place(s, plan.z));
+                if (p.dout.p) PY::fetch(at.of<const Y>(p.dout), l, d, place(s, plan.dout));
+                if (RES) PR::fetch(at.of<const R>(p.res), l, d, place(s, plan.r));
+                if (RES && p.drout.p) PR::fetch(at.of<const R>(p.drout), l, d, place(s, plan.dr));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t base = (int64_t)blockIdx.x * ROWS;
+    fetch(base, 0);
+    for (; base < p.rows; base += step, s ^= 1) {
+        fetch(base + step, s ^ 1);
+        if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int64_t row = base + threadIdx.x / TPR;
+        const bool on = row < p.rows;
+        const int dd = on ? d : 0;
+        const RowAt at(p, on ? (unsigned)row : 0u);
+        float y[8], y1[8], a[8], da[8], dv[8], w[8];
+        auto get_y = [&](int k, const RowRef& ref, float* f) {
+            if constexpr (VEC) PY::take(place(s, k), l, dd, f);
+            else PY::load(at.of<const Y>(ref), l, dd, f);
+        };
+        auto get_r = [&](int k, const RowRef& ref, float* f) {
+            if constexpr (VEC) PR::take(place(s, k), l, dd, f);
+            else PR::load(at.of<const R>(ref), l, dd, f);
+        };
+        get_y(0, p.y, y);
+        float rstd1 = 1.f;
+        if (p.w.p) {
+            float q = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(y[e], y[e], q);
+            row_sum<TPR, 1>(&q, sh, turn);
+            rstd1 = on ? rsqrtf(q * inv + p.eps) : 0.f;    // no row: nothing into the sums
+            param_part<TPR, VEC>(p.w, l, d, 1.f, w);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y1[e] = p.w.p ? y[e] * (rstd1 * w[e]) : y[e];
+        if (p.gate.p) {
+            get_y(plan.z, p.gate, a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = norm_act(a[e], p.act, &da[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = 1.f;
+        }
+        if constexpr (!RES) {
+            get_y(plan.dout, p.dout, dv);
+        } else {
+            float sc[8];
+            param_part<TPR, VEC>(p.sc, l, d, 1.f, sc);
+            if (p.drout.p) {
+                get_r(plan.dr, p.drout, dv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dv[e] = 0.f;
+            }
+            if (p.nw.p) {
+                float r[8], dn[8], t[8];
+                get_r(plan.r, p.res, r);
+                get_y(plan.dout, p.dout, dn);
+                param_part<TPR, VEC>(p.nw, l, d, 1.f, t);
+                float v[2] = {0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    r[e] = fmaf(sc[e], y1[e] * a[e], r[e]);
+                    t[e] *= dn[e];
+                    v[0] = fmaf(r[e], r[e], v[0]);
+                    v[1] = fmaf(t[e], r[e], v[1]);
+                }
+                row_sum<TPR, 2>(v, sh, turn);
+                const float rstd2 = on ? rsqrtf(v[0] * inv + p.eps) : 0.f;
+                const float m2 = v[1] * inv * rstd2 * rstd2;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    an[e] = fmaf(dn[e], r[e] * rstd2, an[e]);
+                    dv[e] = fmaf(rstd2, fmaf(-r[e], m2, t[e]), dv[e]);
+                }
+            }
+            if (on) PR::store(at.of<R>(p.dres), l, d, dv);
+            if (p.sc.p)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    as[e] = fmaf(dv[e], y1[e] * a[e], as[e]);
+                    dv[e] *= sc[e];
+                }
+        }
+        if (p.gate.p) {
+            float dz[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dz[e] = dv[e] * y1[e] * da[e];
+                dv[e] *= a[e];
+            }
+            if (on) PY::store(at.of<Y>(p.dgate), l, d, dz);
+        }
+        if (p.w.p) {
+            float c = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                aw[e] = fmaf(dv[e], y[e] * rstd1, aw[e]);
+                dv[e] *= w[e];
+                c = fmaf(dv[e], y[e], c);
+            }
+            row_sum<TPR, 1>(&c, sh, turn);
+            const float m1 = c * inv * rstd1 * rstd1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dv[e] = rstd1 * fmaf(-y[e], m1, dv[e]);
+        }
+        if (on) PY::store(at.of<Y>(p.dy), l, d, dv);
+    }
+    if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!p.part) return;
+    // this CTA's partial sums: its groups of rows in order
+    float* part = p.part + (int64_t)blockIdx.x * 3 * d;
+    auto put = [&](int k, const float* acc) {
+        if constexpr (ROWS == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = RowPart<float, TPR, VEC>::col(l, e);
+                if (c < d) part[k * d + c] = acc[e];
+            }
+        } else {
+            __shared__ float group[ROWS][TPR * 8];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) group[threadIdx.x / TPR][RowPart<float, TPR, VEC>::col(l, e)] = acc[e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < d; c += TH) {
+                float t = 0.f;
+                for (int g = 0; g < ROWS; ++g) t += group[g][c];
+                part[k * d + c] = t;
+            }
+        }
+    };
+    if (p.w.p) put(0, aw);
+    if (p.sc.p) put(1, as);
+    if (p.nw.p) put(2, an);
+}
+
+// ---- longer rows: element by element, the row read again for each sum --------------------
 
 template <typename Y, typename R>
 __global__ void __launch_bounds__(kNormThreads) k_norm_fwd(NormParams p) {

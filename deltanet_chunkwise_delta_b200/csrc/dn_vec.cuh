@@ -83,6 +83,7 @@ __device__ __forceinline__ void st_vec(E* p, const float* f) {
 struct ParamVec {
     const void* p;  // null: not given
     int bf16;
+    int vec;        // 16-byte aligned
 };
 __device__ __forceinline__ float ld_param(const ParamVec& v, int j) {
     return v.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v.p)[j])
