@@ -102,6 +102,14 @@ void norm_collapse(NormParams& p) {
     }
 }
 
+// Whether every tensor has y's row strides.
+int norm_same(const NormParams& p) {
+    const RowRef* refs[] = {&p.gate, &p.res, &p.out, &p.rout, &p.dout, &p.drout, &p.dy, &p.dgate, &p.dres};
+    for (const RowRef* r : refs)
+        if (r->p && (r->s0 != p.y.s0 || (p.n1 > 1 && r->s1 != p.y.s1) || (p.n2 > 1 && r->s2 != p.y.s2))) return 0;
+    return 1;
+}
+
 // Every row of every tensor starts on 16 bytes.
 bool norm_wide(const NormParams& p, int ysize, int rsize) {
     const RowRef* ys[] = {&p.y, &p.gate, &p.out, &p.dout, &p.dy, &p.dgate};
@@ -137,6 +145,14 @@ bool norm_smem(Kern* kern, int bytes) {
            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
+// CTAs of a kernel that the GPU holds at once (they walk the rows, so more would only queue).
+template <typename Kern>
+int norm_resident(Kern* kern, int threads, int smem, int sms) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) n = 1;
+    return n * sms;
+}
+
 template <typename Y, typename R, bool RES>
 dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t stream) {
     bool ok = true;
@@ -144,24 +160,28 @@ dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t str
         constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
         constexpr bool VEC = decltype(vec)::value;
         const int64_t need = (p.rows + ROWS - 1) / ROWS;
-        const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)sms * (2048 / TH));
         const int smem = VEC ? 2 * NormPlan<Y, R>(p).all * TH * 16 : 0;
         auto* kern = k_norm_fwd_rows<Y, R, TPR, VEC, RES>;
-        if ((ok = norm_smem(kern, smem))) kern<<<grid, TH, smem, stream>>>(p);
+        if (!(ok = norm_smem(kern, smem))) return;
+        const int64_t grid = need > sms ? std::min<int64_t>(need, norm_resident(kern, TH, smem, sms)) : need;
+        kern<<<(unsigned)grid, TH, smem, stream>>>(p);
     });
     if (!done) k_norm_fwd<Y, R><<<(unsigned)p.rows, kNormThreads, 0, stream>>>(p);
     return ok ? launched(1) : DN_ERR_CUDA;
 }
 
 template <typename Y, typename R, bool RES>
-dn_status norm_bwd_run(const NormParams& p, bool wide, int ctas, cudaStream_t stream) {
+dn_status norm_bwd_run(const NormParams& p, bool wide, int sms, int& ctas, cudaStream_t stream) {
     bool ok = true;
     const bool done = norm_by_length(p.d, wide, [&](auto tpr, auto vec) {
-        constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>;
+        constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
         constexpr bool VEC = decltype(vec)::value;
         const int smem = VEC ? 2 * NormPlan<Y, R>(p).all * TH * 16 : 0;
         auto* kern = k_norm_bwd_rows<Y, R, TPR, VEC, RES>;
-        if ((ok = norm_smem(kern, smem))) kern<<<ctas, TH, smem, stream>>>(p);
+        if (!(ok = norm_smem(kern, smem))) return;
+        ctas = (int)std::min<int64_t>(ctas, (p.rows + ROWS - 1) / ROWS);
+        if (ctas > sms) ctas = std::min(ctas, norm_resident(kern, TH, smem, sms));
+        kern<<<ctas, TH, smem, stream>>>(p);
     });
     if (!done) {
         auto* kern = k_norm_bwd<Y, R>;
@@ -207,6 +227,7 @@ dn_status deltanet_norm_fwd(const dn_tensor* y, const dn_tensor* weight, const d
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
     norm_collapse(p);
+    p.same = norm_same(p);
     return norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
         return norm_fwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, stream);
     });
@@ -260,13 +281,14 @@ dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const d
     p.dres = row_ref(d_residual);
     p.part = need > 0 ? static_cast<float*>(workspace->data) : nullptr;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-    const int ctas = norm_bwd_ctas(p.rows);
+    int ctas = norm_bwd_ctas(p.rows);
     int launches = 0;
     if (p.rows > 0) {
         const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
         norm_collapse(p);
+        p.same = norm_same(p);
         st = norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
-            return norm_bwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, ctas, stream);
+            return norm_bwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, ctas, stream);
         });
         if (st != DN_OK) return st;
         ++launches;

@@ -36,8 +36,36 @@ struct NormParams {
     float eps;
     int64_t rows;
     unsigned n1, n2;                   // row = (i0 * n1 + i1) * n2 + i2
+    int same;                          // every tensor has y's strides
     int d;
 };
+
+// On pairs of the 8 elements of a thread: one instruction for two.
+__device__ __forceinline__ void mul8(const float* a, const float* b, float* d) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(a + e, b + e, d + e);
+}
+__device__ __forceinline__ void mul8(const float* a, float b, float* d) {
+    const float bb[2] = {b, b};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(a + e, bb, d + e);
+}
+__device__ __forceinline__ void fma8(const float* a, const float* b, const float* c, float* d) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) fma2(a + e, b + e, c + e, d + e);
+}
+__device__ __forceinline__ void fma8(const float* a, float b, const float* c, float* d) {
+    const float bb[2] = {b, b};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) fma2(a + e, bb, c + e, d + e);
+}
+// sum of a b
+__device__ __forceinline__ float dot8(const float* a, const float* b) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) fma2(a + e, b + e, s, s);
+    return s[0] + s[1];
+}
 
 template <typename E>
 __device__ __forceinline__ E* row_ptr(const RowRef& r, unsigned i0, unsigned i1, unsigned i2) {
@@ -199,16 +227,22 @@ __device__ __forceinline__ void param_part(const ParamVec& v, int l, int d, floa
     }
 }
 
+// Where a row is: in a tensor with y's strides, or in any.
 struct RowAt {
     unsigned i0, i1, i2;
-    __device__ __forceinline__ RowAt(const NormParams& p, unsigned row) {
+    int64_t off;
+    bool same;
+    __device__ __forceinline__ RowAt(const NormParams& p, unsigned row) : same(p.same) {
         const unsigned q = p.n2 == 1 ? row : row / p.n2;
         i2 = row - q * p.n2;
         i0 = p.n1 == 1 ? q : q / p.n1;
         i1 = q - i0 * p.n1;
+        off = i0 * p.y.s0 + i1 * p.y.s1 + i2 * p.y.s2;
     }
     template <typename E>
-    __device__ __forceinline__ E* of(const RowRef& r) const { return row_ptr<E>(r, i0, i1, i2); }
+    __device__ __forceinline__ E* of(const RowRef& r) const {
+        return same ? static_cast<E*>(const_cast<void*>(r.p)) + off : row_ptr<E>(r, i0, i1, i2);
+    }
 };
 
 // Rounds of 16 bytes per thread in shared memory: where each operand's begin, and their number.
@@ -231,7 +265,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
     using PR = RowPart<R, TPR, VEC>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
     extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
-    __shared__ float sh[2][2][32];
+    __shared__ __align__(16) float sh[2][2][32];
     const NormPlan<Y, R> plan(p);
     auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
     const int l = threadIdx.x % TPR, d = p.d;
@@ -276,13 +310,10 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
             if (RES) PR::load(at.of<const R>(p.res), l, dd, r);
         }
         if (p.w.p) {
-            float q = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+            float q = dot8(v, v);
             row_sum<TPR, 1>(&q, sh, turn);
-            const float rstd = rsqrtf(q * inv + p.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= rstd * w[e];
+            mul8(v, rsqrtf(q * inv + p.eps), v);
+            mul8(v, w, v);
         }
         if (p.gate.p)
 #pragma unroll
@@ -290,17 +321,13 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
         if constexpr (!RES) {
             if (on) PY::store(at.of<Y>(p.out), l, d, v);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(sc[e], v[e], r[e]);
+            fma8(v, sc, r, v);
             if (on) PR::store(at.of<R>(p.rout), l, d, v);
             if (p.nw.p) {
-                float q = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+                float q = dot8(v, v);
                 row_sum<TPR, 1>(&q, sh, turn);
-                const float rstd = rsqrtf(q * inv + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= rstd * nw[e];
+                mul8(v, rsqrtf(q * inv + p.eps), v);
+                mul8(v, nw, v);
                 if (on) PY::store(at.of<Y>(p.out), l, d, v);
             }
         }
@@ -314,7 +341,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
     using PR = RowPart<R, TPR, VEC>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
     extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
-    __shared__ float sh[2][2][32];
+    __shared__ __align__(16) float sh[2][2][32];
     const NormPlan<Y, R> plan(p);
     auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
     const int l = threadIdx.x % TPR, d = p.d;
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
         const bool on = row < p.rows;
         const int dd = on ? d : 0;
         const RowAt at(p, on ? (unsigned)row : 0u);
-        float y[8], y1[8], a[8], da[8], dv[8], w[8];
+        float y[8], y1[8], a[8], da[8], dv[8], w[8];   // y: y rstd1 from the first sum on
         auto get_y = [&](int k, const RowRef& ref, float* f) {
             if constexpr (VEC) PY::take(place(s, k), l, dd, f);
             else PY::load(at.of<const Y>(ref), l, dd, f);
@@ -357,22 +384,22 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
         get_y(0, p.y, y);
         float rstd1 = 1.f;
         if (p.w.p) {
-            float q = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q = fmaf(y[e], y[e], q);
+            float q = dot8(y, y);
             row_sum<TPR, 1>(&q, sh, turn);
             rstd1 = on ? rsqrtf(q * inv + p.eps) : 0.f;    // no row: nothing into the sums
             param_part<TPR, VEC>(p.w, l, d, 1.f, w);
-        }
+            mul8(y, rstd1, y);
+            mul8(y, w, y1);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y1[e] = p.w.p ? y[e] * (rstd1 * w[e]) : y[e];
+            for (int e = 0; e < 8; ++e) y1[e] = y[e];
+        }
         if (p.gate.p) {
             get_y(plan.z, p.gate, a);
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] = norm_act(a[e], p.act, &da[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] = 1.f;
+            mul8(da, y1, da);                              // what dy2 is worth to the gate
+            mul8(y1, a, y1);                               // y2
         }
         if constexpr (!RES) {
             get_y(plan.dout, p.dout, dv);
@@ -390,52 +417,35 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
                 get_r(plan.r, p.res, r);
                 get_y(plan.dout, p.dout, dn);
                 param_part<TPR, VEC>(p.nw, l, d, 1.f, t);
-                float v[2] = {0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    r[e] = fmaf(sc[e], y1[e] * a[e], r[e]);
-                    t[e] *= dn[e];
-                    v[0] = fmaf(r[e], r[e], v[0]);
-                    v[1] = fmaf(t[e], r[e], v[1]);
-                }
+                fma8(sc, y1, r, r);
+                mul8(t, dn, t);
+                float v[2] = {dot8(r, r), dot8(t, r)};
                 row_sum<TPR, 2>(v, sh, turn);
                 const float rstd2 = on ? rsqrtf(v[0] * inv + p.eps) : 0.f;
-                const float m2 = v[1] * inv * rstd2 * rstd2;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    an[e] = fmaf(dn[e], r[e] * rstd2, an[e]);
-                    dv[e] = fmaf(rstd2, fmaf(-r[e], m2, t[e]), dv[e]);
-                }
+                const float m2 = -v[1] * inv * rstd2 * rstd2;
+                fma8(r, m2, t, t);
+                fma8(t, rstd2, dv, dv);
+                mul8(r, rstd2, r);
+                fma8(dn, r, an, an);
             }
             if (on) PR::store(at.of<R>(p.dres), l, d, dv);
-            if (p.sc.p)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    as[e] = fmaf(dv[e], y1[e] * a[e], as[e]);
-                    dv[e] *= sc[e];
-                }
+            if (p.sc.p) {
+                fma8(dv, y1, as, as);
+                mul8(dv, sc, dv);
+            }
         }
         if (p.gate.p) {
-            float dz[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dz[e] = dv[e] * y1[e] * da[e];
-                dv[e] *= a[e];
-            }
-            if (on) PY::store(at.of<Y>(p.dgate), l, d, dz);
+            mul8(da, dv, da);
+            mul8(dv, a, dv);
+            if (on) PY::store(at.of<Y>(p.dgate), l, d, da);
         }
         if (p.w.p) {
-            float c = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                aw[e] = fmaf(dv[e], y[e] * rstd1, aw[e]);
-                dv[e] *= w[e];
-                c = fmaf(dv[e], y[e], c);
-            }
+            fma8(dv, y, aw, aw);
+            mul8(dv, w, dv);
+            float c = dot8(dv, y);
             row_sum<TPR, 1>(&c, sh, turn);
-            const float m1 = c * inv * rstd1 * rstd1;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dv[e] = rstd1 * fmaf(-y[e], m1, dv[e]);
+            fma8(y, -c * inv, dv, dv);                     // y holds one rstd1, the factor after it the others
+            mul8(dv, rstd1, dv);
         }
         if (on) PY::store(at.of<Y>(p.dy), l, d, dv);
     }

@@ -510,26 +510,6 @@ struct ScanSrc {
     }
 };
 
-// Two channels in one instruction.
-__device__ __forceinline__ void fma2(const float* a, const float* b, const float* c, float* d) {
-    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
-        "  fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
-        : "=f"(d[0]), "=f"(d[1])
-        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
-}
-__device__ __forceinline__ void add2(const float* a, const float* b, float* d) {
-    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
-        "  add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
-        : "=f"(d[0]), "=f"(d[1])
-        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
-}
-__device__ __forceinline__ void mul2(const float* a, const float* b, float* d) {
-    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
-        "  mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
-        : "=f"(d[0]), "=f"(d[1])
-        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
-}
-
 // e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
 // relative in all, where a token's step needs no more: a decay's error enters h with weight a.
 __device__ __forceinline__ void scan_log2(float* g) {

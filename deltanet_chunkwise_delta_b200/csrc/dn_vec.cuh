@@ -79,6 +79,26 @@ __device__ __forceinline__ void st_vec(E* p, const float* f) {
     *reinterpret_cast<typename RawVec<E, V>::T*>(p) = r;
 }
 
+// Two fp32 operations in one instruction (pairs of neighbours; d may be an operand).
+__device__ __forceinline__ void fma2(const float* a, const float* b, const float* c, float* d) {
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+        "  fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void add2(const float* a, const float* b, float* d) {
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+        "  add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+__device__ __forceinline__ void mul2(const float* a, const float* b, float* d) {
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+        "  mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+
 // A [d] parameter vector in fp32 or bf16.
 struct ParamVec {
     const void* p;  // null: not given
