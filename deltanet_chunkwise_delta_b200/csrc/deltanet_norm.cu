@@ -103,11 +103,11 @@ void norm_collapse(NormParams& p) {
 }
 
 // Whether every tensor has y's row strides.
-int norm_same(const NormParams& p) {
+bool norm_same(const NormParams& p) {
     const RowRef* refs[] = {&p.gate, &p.res, &p.out, &p.rout, &p.dout, &p.drout, &p.dy, &p.dgate, &p.dres};
     for (const RowRef* r : refs)
-        if (r->p && (r->s0 != p.y.s0 || (p.n1 > 1 && r->s1 != p.y.s1) || (p.n2 > 1 && r->s2 != p.y.s2))) return 0;
-    return 1;
+        if (r->p && (r->s0 != p.y.s0 || (p.n1 > 1 && r->s1 != p.y.s1) || (p.n2 > 1 && r->s2 != p.y.s2))) return false;
+    return true;
 }
 
 // Every row of every tensor starts on 16 bytes.
@@ -123,20 +123,23 @@ bool norm_wide(const NormParams& p, int ysize, int rsize) {
     return w;
 }
 
-// Threads of a row by its length: f(integral_constant<TPR>, bool_constant<VEC>); false past the
-// longest row that is held in registers.
-template <int TPR, bool VEC, typename F>
+// Threads of a row by its length: f(integral_constant<TPR>, bool_constant<VEC>,
+// bool_constant<SAME>); false past the longest row that is held in registers.
+template <int TPR, bool VEC, bool SAME, typename F>
 bool norm_try(int d, F& f) {
     if (d > TPR * 8) return false;
-    f(std::integral_constant<int, TPR>(), std::bool_constant<VEC>());
+    f(std::integral_constant<int, TPR>(), std::bool_constant<VEC>(), std::bool_constant<SAME>());
     return true;
 }
+template <bool SAME, typename F>
+bool norm_by_length(int d, F& f) {
+    return norm_try<8, true, SAME>(d, f) || norm_try<16, true, SAME>(d, f) || norm_try<32, true, SAME>(d, f) ||
+           norm_try<128, true, SAME>(d, f) || norm_try<256, true, SAME>(d, f) || norm_try<512, true, SAME>(d, f);
+}
 template <typename F>
-bool norm_by_length(int d, bool wide, F f) {
-    if (wide)
-        return norm_try<8, true>(d, f) || norm_try<16, true>(d, f) || norm_try<32, true>(d, f) ||
-               norm_try<128, true>(d, f) || norm_try<256, true>(d, f) || norm_try<512, true>(d, f);
-    return norm_try<32, false>(d, f) || norm_try<128, false>(d, f) || norm_try<512, false>(d, f);
+bool norm_by_length(const NormParams& p, bool wide, F f) {
+    if (wide) return norm_same(p) ? norm_by_length<true>(p.d, f) : norm_by_length<false>(p.d, f);
+    return norm_try<32, false, false>(p.d, f) || norm_try<128, false, false>(p.d, f) || norm_try<512, false, false>(p.d, f);
 }
 
 template <typename Kern>
@@ -156,12 +159,12 @@ int norm_resident(Kern* kern, int threads, int smem, int sms) {
 template <typename Y, typename R, bool RES>
 dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t stream) {
     bool ok = true;
-    const bool done = norm_by_length(p.d, wide, [&](auto tpr, auto vec) {
+    const bool done = norm_by_length(p, wide, [&](auto tpr, auto vec, auto same) {
         constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
         constexpr bool VEC = decltype(vec)::value;
         const int64_t need = (p.rows + ROWS - 1) / ROWS;
-        const int smem = VEC ? 2 * NormPlan<Y, R>(p).all * TH * 16 : 0;
-        auto* kern = k_norm_fwd_rows<Y, R, TPR, VEC, RES>;
+        constexpr int smem = VEC ? 2 * NormPlan<Y, R, RES, false>::all * TH * 16 : 0;
+        auto* kern = k_norm_fwd_rows<Y, R, TPR, VEC, RES, decltype(same)::value>;
         if (!(ok = norm_smem(kern, smem))) return;
         const int64_t grid = need > sms ? std::min<int64_t>(need, norm_resident(kern, TH, smem, sms)) : need;
         kern<<<(unsigned)grid, TH, smem, stream>>>(p);
@@ -173,11 +176,11 @@ dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t str
 template <typename Y, typename R, bool RES>
 dn_status norm_bwd_run(const NormParams& p, bool wide, int sms, int& ctas, cudaStream_t stream) {
     bool ok = true;
-    const bool done = norm_by_length(p.d, wide, [&](auto tpr, auto vec) {
+    const bool done = norm_by_length(p, wide, [&](auto tpr, auto vec, auto same) {
         constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
         constexpr bool VEC = decltype(vec)::value;
-        const int smem = VEC ? 2 * NormPlan<Y, R>(p).all * TH * 16 : 0;
-        auto* kern = k_norm_bwd_rows<Y, R, TPR, VEC, RES>;
+        constexpr int smem = ((VEC ? 2 * NormPlan<Y, R, RES, true>::all : 0) + (RES ? 6 : 2)) * TH * 16;
+        auto* kern = k_norm_bwd_rows<Y, R, TPR, VEC, RES, decltype(same)::value>;
         if (!(ok = norm_smem(kern, smem))) return;
         ctas = (int)std::min<int64_t>(ctas, (p.rows + ROWS - 1) / ROWS);
         if (ctas > sms) ctas = std::min(ctas, norm_resident(kern, TH, smem, sms));
@@ -227,7 +230,6 @@ dn_status deltanet_norm_fwd(const dn_tensor* y, const dn_tensor* weight, const d
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
     norm_collapse(p);
-    p.same = norm_same(p);
     return norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
         return norm_fwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, stream);
     });
@@ -286,7 +288,6 @@ dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const d
     if (p.rows > 0) {
         const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
         norm_collapse(p);
-        p.same = norm_same(p);
         st = norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
             return norm_bwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, ctas, stream);
         });

@@ -36,7 +36,6 @@ struct NormParams {
     float eps;
     int64_t rows;
     unsigned n1, n2;                   // row = (i0 * n1 + i1) * n2 + i2
-    int same;                          // every tensor has y's strides
     int d;
 };
 
@@ -176,7 +175,6 @@ struct RowPart {
     }
     __device__ static __forceinline__ void store(E* row, int l, int d, const float* f) {
         if constexpr (VEC) {
-            if (l * 8 >= d) return;
             if constexpr (sizeof(E) == 2) {
                 uint32_t u[4];
 #pragma unroll
@@ -194,17 +192,14 @@ struct RowPart {
         }
     }
     // this thread's pieces into shared memory (16 bytes a thread side by side), and from there
-    __device__ static __forceinline__ void fetch(const E* row, int l, int d, uint4* place) {
-        if (l * 8 < d)
+    __device__ static __forceinline__ void fetch(const E* piece, uint4* place) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                cp_async16(place + i * kNormCta<TPR>, reinterpret_cast<const uint4*>(row + l * 8) + i);
+        for (int i = 0; i < kPieces; ++i) cp_async16(place + i * kNormCta<TPR>, reinterpret_cast<const uint4*>(piece) + i);
     }
-    __device__ static __forceinline__ void take(const uint4* place, int l, int d, float* f) {
-        uint4 q[kPieces] = {};
-        if (l * 8 < d)
+    __device__ static __forceinline__ void take(const uint4* place, float* f) {
+        uint4 q[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) q[i] = place[i * kNormCta<TPR>];
+        for (int i = 0; i < kPieces; ++i) q[i] = place[i * kNormCta<TPR>];
         unpack16(q, f);
     }
 };
@@ -227,48 +222,41 @@ __device__ __forceinline__ void param_part(const ParamVec& v, int l, int d, floa
     }
 }
 
-// Where a row is: in a tensor with y's strides, or in any.
+// Where a row is: every tensor has y's strides (SAME), or each its own.
+template <bool SAME>
 struct RowAt {
-    unsigned i0, i1, i2;
-    int64_t off;
-    bool same;
-    __device__ __forceinline__ RowAt(const NormParams& p, unsigned row) : same(p.same) {
+    unsigned i0 = 0, i1 = 0, i2 = 0;
+    int64_t off = 0;
+    __device__ __forceinline__ RowAt(const NormParams& p, unsigned row) {
         const unsigned q = p.n2 == 1 ? row : row / p.n2;
         i2 = row - q * p.n2;
         i0 = p.n1 == 1 ? q : q / p.n1;
         i1 = q - i0 * p.n1;
-        off = i0 * p.y.s0 + i1 * p.y.s1 + i2 * p.y.s2;
+        if (SAME) off = i0 * p.y.s0 + i1 * p.y.s1 + i2 * p.y.s2;
     }
     template <typename E>
     __device__ __forceinline__ E* of(const RowRef& r) const {
-        return same ? static_cast<E*>(const_cast<void*>(r.p)) + off : row_ptr<E>(r, i0, i1, i2);
+        return SAME ? static_cast<E*>(const_cast<void*>(r.p)) + off : row_ptr<E>(r, i0, i1, i2);
     }
 };
 
 // Rounds of 16 bytes per thread in shared memory: where each operand's begin, and their number.
-template <typename Y, typename R>
+template <typename Y, typename R, bool RES, bool BWD>
 struct NormPlan {
-    int z, dout, r, dr, all;
-    __host__ __device__ NormPlan(const NormParams& p) {
-        constexpr int nY = sizeof(Y) / 2, nR = sizeof(R) / 2;
-        z = nY;
-        dout = z + (p.gate.p ? nY : 0);
-        r = dout + (p.dout.p ? nY : 0);
-        dr = r + (p.res.p ? nR : 0);
-        all = dr + (p.drout.p ? nR : 0);
-    }
+    static constexpr int nY = sizeof(Y) / 2, nR = RES ? (int)sizeof(R) / 2 : 0;
+    static constexpr int z = nY, dout = 2 * nY, r = dout + (BWD ? nY : 0), dr = r + nR, all = dr + (BWD ? nR : 0);
 };
 
-template <typename Y, typename R, int TPR, bool VEC, bool RES>
+template <typename Y, typename R, int TPR, bool VEC, bool RES, bool SAME>
 __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
     using PY = RowPart<Y, TPR, VEC>;
     using PR = RowPart<R, TPR, VEC>;
+    using Plan = NormPlan<Y, R, RES, false>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
-    extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
+    extern __shared__ uint4 ring_mem[];                // [2][Plan::all][TH], with VEC
     __shared__ __align__(16) float sh[2][2][32];
-    const NormPlan<Y, R> plan(p);
-    auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
     const int l = threadIdx.x % TPR, d = p.d;
+    const bool part = !VEC || l * 8 < d;               // VEC: this thread has elements
     int turn = 0, s = 0;
     const float inv = 1.f / (float)d;
     float w[8], sc[8], nw[8];
@@ -277,37 +265,39 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
         param_part<TPR, VEC>(p.sc, l, d, 1.f, sc);
         param_part<TPR, VEC>(p.nw, l, d, 1.f, nw);
     }
-    auto fetch = [&](int64_t base, int s) {
+    if (VEC)                                           // what is never fetched reads as zeros
+        for (int i = 0; i < 2 * Plan::all; ++i) ring_mem[i * TH + threadIdx.x] = make_uint4(0, 0, 0, 0);
+    auto place = [&](int s, int k) { return ring_mem + ((s * Plan::all + k) * TH + threadIdx.x); };
+    auto fetch = [&](const RowAt<SAME>& at, bool on, int s) {
         if constexpr (VEC) {
-            const int64_t row = base + threadIdx.x / TPR;
-            if (row < p.rows) {
-                const RowAt at(p, (unsigned)row);
-                PY::fetch(at.of<const Y>(p.y), l, d, place(s, 0));
-                if (p.gate.p) PY::fetch(at.of<const Y>(p.gate), l, d, place(s, plan.z));
-                if (RES) PR::fetch(at.of<const R>(p.res), l, d, place(s, plan.r));
+            if (on) {
+                PY::fetch(at.template of<const Y>(p.y) + l * 8, place(s, 0));
+                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate) + l * 8, place(s, Plan::z));
+                if (RES) PR::fetch(at.template of<const R>(p.res) + l * 8, place(s, Plan::r));
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    int64_t base = (int64_t)blockIdx.x * ROWS;
-    fetch(base, 0);
+    int64_t base = (int64_t)blockIdx.x * ROWS, row = base + threadIdx.x / TPR;
+    RowAt<SAME> at(p, row < p.rows ? (unsigned)row : 0u);
+    fetch(at, part && row < p.rows, 0);
     for (; base < p.rows; base += step, s ^= 1) {
-        fetch(base + step, s ^ 1);
+        const bool on = part && row < p.rows;          // what a row past the last computes is not stored
+        row += step;
+        const RowAt<SAME> next(p, row < p.rows ? (unsigned)row : 0u);
+        fetch(next, part && row < p.rows, s ^ 1);
         if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const int64_t row = base + threadIdx.x / TPR;
-        const bool on = row < p.rows;
-        const int dd = on ? d : 0;                     // rows past the last: no elements
-        const RowAt at(p, on ? (unsigned)row : 0u);
         float v[8], z[8], r[8];
         if constexpr (VEC) {
-            PY::take(place(s, 0), l, dd, v);
-            if (p.gate.p) PY::take(place(s, plan.z), l, dd, z);
-            if (RES) PR::take(place(s, plan.r), l, dd, r);
+            PY::take(place(s, 0), v);
+            if (p.gate.p) PY::take(place(s, Plan::z), z);
+            if (RES) PR::take(place(s, Plan::r), r);
         } else {
-            PY::load(at.of<const Y>(p.y), l, dd, v);
-            if (p.gate.p) PY::load(at.of<const Y>(p.gate), l, dd, z);
-            if (RES) PR::load(at.of<const R>(p.res), l, dd, r);
+            const int dd = on ? d : 0;
+            PY::load(at.template of<const Y>(p.y), l, dd, v);
+            if (p.gate.p) PY::load(at.template of<const Y>(p.gate), l, dd, z);
+            if (RES) PR::load(at.template of<const R>(p.res), l, dd, r);
         }
         if (p.w.p) {
             float q = dot8(v, v);
@@ -319,75 +309,104 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= norm_act(z[e], p.act);
         if constexpr (!RES) {
-            if (on) PY::store(at.of<Y>(p.out), l, d, v);
+            if (on) PY::store(at.template of<Y>(p.out), l, d, v);
         } else {
             fma8(v, sc, r, v);
-            if (on) PR::store(at.of<R>(p.rout), l, d, v);
+            if (on) PR::store(at.template of<R>(p.rout), l, d, v);
             if (p.nw.p) {
                 float q = dot8(v, v);
                 row_sum<TPR, 1>(&q, sh, turn);
                 mul8(v, rsqrtf(q * inv + p.eps), v);
                 mul8(v, nw, v);
-                if (on) PY::store(at.of<Y>(p.out), l, d, v);
+                if (on) PY::store(at.template of<Y>(p.out), l, d, v);
             }
         }
+        at = next;
     }
     if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename Y, typename R, int TPR, bool VEC, bool RES>
+// The parameters stay in shared memory in fp32 (a thread's 8 by pairs of float4, as the ring).
+template <int TPR, bool VEC>
+__device__ __forceinline__ void param_take(const float4* mem, int k, float* f) {
+    constexpr int TH = kNormCta<TPR>;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 q = mem[(k * 2 + i) * TH + threadIdx.x];
+        f[4 * i] = q.x;
+        f[4 * i + 1] = q.y;
+        f[4 * i + 2] = q.z;
+        f[4 * i + 3] = q.w;
+    }
+}
+
+template <typename Y, typename R, int TPR, bool VEC, bool RES, bool SAME>
 __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
     using PY = RowPart<Y, TPR, VEC>;
     using PR = RowPart<R, TPR, VEC>;
+    using Plan = NormPlan<Y, R, RES, true>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
-    extern __shared__ uint4 ring_mem[];                // [2][plan.all][TH], with VEC
+    extern __shared__ uint4 ring_mem[];                // parameters, then [2][Plan::all][TH], with VEC
     __shared__ __align__(16) float sh[2][2][32];
-    const NormPlan<Y, R> plan(p);
-    auto place = [&](int s, int k) { return ring_mem + ((s * plan.all + k) * TH + threadIdx.x); };
     const int l = threadIdx.x % TPR, d = p.d;
+    const bool part = !VEC || l * 8 < d;
     int turn = 0, s = 0;
     const float inv = 1.f / (float)d;
     float aw[8] = {}, as[8] = {}, an[8] = {};          // sums over this thread's rows
-    auto fetch = [&](int64_t base, int s) {
+    float4* const par = reinterpret_cast<float4*>(ring_mem);
+    auto keep = [&](int k, const ParamVec& v) {
+        float f[8];
+        param_part<TPR, VEC>(v, l, d, 1.f, f);
+        par[(k * 2) * TH + threadIdx.x] = make_float4(f[0], f[1], f[2], f[3]);
+        par[(k * 2 + 1) * TH + threadIdx.x] = make_float4(f[4], f[5], f[6], f[7]);
+    };
+    keep(0, p.w);
+    if (RES) keep(1, p.sc), keep(2, p.nw);
+    uint4* const ring = ring_mem + (RES ? 6 : 2) * TH;
+    auto place = [&](int s, int k) { return ring + ((s * Plan::all + k) * TH + threadIdx.x); };
+    if (VEC)                                           // what is never fetched reads as zeros
+        for (int i = 0; i < 2 * Plan::all; ++i) ring[i * TH + threadIdx.x] = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](const RowAt<SAME>& at, bool on, int s) {
         if constexpr (VEC) {
-            const int64_t row = base + threadIdx.x / TPR;
-            if (row < p.rows) {
-                const RowAt at(p, (unsigned)row);
-                PY::fetch(at.of<const Y>(p.y), l, d, place(s, 0));
-                if (p.gate.p) PY::fetch(at.of<const Y>(p.gate), l, d, place(s, plan.z));
-                if (p.dout.p) PY::fetch(at.of<const Y>(p.dout), l, d, place(s, plan.dout));
-                if (RES) PR::fetch(at.of<const R>(p.res), l, d, place(s, plan.r));
-                if (RES && p.drout.p) PR::fetch(at.of<const R>(p.drout), l, d, place(s, plan.dr));
+            if (on) {
+                PY::fetch(at.template of<const Y>(p.y) + l * 8, place(s, 0));
+                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate) + l * 8, place(s, Plan::z));
+                if (p.dout.p) PY::fetch(at.template of<const Y>(p.dout) + l * 8, place(s, Plan::dout));
+                if (RES) PR::fetch(at.template of<const R>(p.res) + l * 8, place(s, Plan::r));
+                if (RES && p.drout.p) PR::fetch(at.template of<const R>(p.drout) + l * 8, place(s, Plan::dr));
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    int64_t base = (int64_t)blockIdx.x * ROWS;
-    fetch(base, 0);
+    int64_t base = (int64_t)blockIdx.x * ROWS, row = base + threadIdx.x / TPR;
+    RowAt<SAME> at(p, row < p.rows ? (unsigned)row : 0u);
+    fetch(at, part && row < p.rows, 0);
     for (; base < p.rows; base += step, s ^= 1) {
-        fetch(base + step, s ^ 1);
+        const bool is = row < p.rows, on = part && is;
+        row += step;
+        const RowAt<SAME> next(p, row < p.rows ? (unsigned)row : 0u);
+        fetch(next, part && row < p.rows, s ^ 1);
         if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const int64_t row = base + threadIdx.x / TPR;
-        const bool on = row < p.rows;
+        if (VEC && ROWS > 1 && !is)                    // past the last row: zeros, nothing into the sums
+            for (int i = 0; i < Plan::all; ++i) *place(s, i) = make_uint4(0, 0, 0, 0);
         const int dd = on ? d : 0;
-        const RowAt at(p, on ? (unsigned)row : 0u);
         float y[8], y1[8], a[8], da[8], dv[8], w[8];   // y: y rstd1 from the first sum on
         auto get_y = [&](int k, const RowRef& ref, float* f) {
-            if constexpr (VEC) PY::take(place(s, k), l, dd, f);
-            else PY::load(at.of<const Y>(ref), l, dd, f);
+            if constexpr (VEC) PY::take(place(s, k), f);
+            else PY::load(at.template of<const Y>(ref), l, dd, f);
         };
         auto get_r = [&](int k, const RowRef& ref, float* f) {
-            if constexpr (VEC) PR::take(place(s, k), l, dd, f);
-            else PR::load(at.of<const R>(ref), l, dd, f);
+            if constexpr (VEC) PR::take(place(s, k), f);
+            else PR::load(at.template of<const R>(ref), l, dd, f);
         };
         get_y(0, p.y, y);
         float rstd1 = 1.f;
         if (p.w.p) {
             float q = dot8(y, y);
             row_sum<TPR, 1>(&q, sh, turn);
-            rstd1 = on ? rsqrtf(q * inv + p.eps) : 0.f;    // no row: nothing into the sums
-            param_part<TPR, VEC>(p.w, l, d, 1.f, w);
+            rstd1 = is ? rsqrtf(q * inv + p.eps) : 0.f;
+            param_take<TPR, VEC>(par, 0, w);
             mul8(y, rstd1, y);
             mul8(y, w, y1);
         } else {
@@ -395,40 +414,40 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
             for (int e = 0; e < 8; ++e) y1[e] = y[e];
         }
         if (p.gate.p) {
-            get_y(plan.z, p.gate, a);
+            get_y(Plan::z, p.gate, a);
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] = norm_act(a[e], p.act, &da[e]);
-            mul8(da, y1, da);                              // what dy2 is worth to the gate
-            mul8(y1, a, y1);                               // y2
+            mul8(da, y1, da);                          // what dy2 is worth to the gate
+            mul8(y1, a, y1);                           // y2
         }
         if constexpr (!RES) {
-            get_y(plan.dout, p.dout, dv);
+            get_y(Plan::dout, p.dout, dv);
         } else {
             float sc[8];
-            param_part<TPR, VEC>(p.sc, l, d, 1.f, sc);
+            param_take<TPR, VEC>(par, 1, sc);
             if (p.drout.p) {
-                get_r(plan.dr, p.drout, dv);
+                get_r(Plan::dr, p.drout, dv);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dv[e] = 0.f;
             }
             if (p.nw.p) {
                 float r[8], dn[8], t[8];
-                get_r(plan.r, p.res, r);
-                get_y(plan.dout, p.dout, dn);
-                param_part<TPR, VEC>(p.nw, l, d, 1.f, t);
+                get_r(Plan::r, p.res, r);
+                get_y(Plan::dout, p.dout, dn);
+                param_take<TPR, VEC>(par, 2, t);
                 fma8(sc, y1, r, r);
                 mul8(t, dn, t);
                 float v[2] = {dot8(r, r), dot8(t, r)};
                 row_sum<TPR, 2>(v, sh, turn);
-                const float rstd2 = on ? rsqrtf(v[0] * inv + p.eps) : 0.f;
+                const float rstd2 = is ? rsqrtf(v[0] * inv + p.eps) : 0.f;
                 const float m2 = -v[1] * inv * rstd2 * rstd2;
                 fma8(r, m2, t, t);
                 fma8(t, rstd2, dv, dv);
                 mul8(r, rstd2, r);
                 fma8(dn, r, an, an);
             }
-            if (on) PR::store(at.of<R>(p.dres), l, d, dv);
+            if (on) PR::store(at.template of<R>(p.dres), l, d, dv);
             if (p.sc.p) {
                 fma8(dv, y1, as, as);
                 mul8(dv, sc, dv);
@@ -437,28 +456,29 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
         if (p.gate.p) {
             mul8(da, dv, da);
             mul8(dv, a, dv);
-            if (on) PY::store(at.of<Y>(p.dgate), l, d, da);
+            if (on) PY::store(at.template of<Y>(p.dgate), l, d, da);
         }
         if (p.w.p) {
             fma8(dv, y, aw, aw);
             mul8(dv, w, dv);
             float c = dot8(dv, y);
             row_sum<TPR, 1>(&c, sh, turn);
-            fma8(y, -c * inv, dv, dv);                     // y holds one rstd1, the factor after it the others
+            fma8(y, -c * inv, dv, dv);                 // y holds one rstd1, the factor after it the others
             mul8(dv, rstd1, dv);
         }
-        if (on) PY::store(at.of<Y>(p.dy), l, d, dv);
+        if (on) PY::store(at.template of<Y>(p.dy), l, d, dv);
+        at = next;
     }
     if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!p.part) return;
     // this CTA's partial sums: its groups of rows in order
-    float* part = p.part + (int64_t)blockIdx.x * 3 * d;
+    float* sums = p.part + (int64_t)blockIdx.x * 3 * d;
     auto put = [&](int k, const float* acc) {
         if constexpr (ROWS == 1) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = RowPart<float, TPR, VEC>::col(l, e);
-                if (c < d) part[k * d + c] = acc[e];
+                if (c < d) sums[k * d + c] = acc[e];
             }
         } else {
             __shared__ float group[ROWS][TPR * 8];
@@ -469,7 +489,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
             for (int c = threadIdx.x; c < d; c += TH) {
                 float t = 0.f;
                 for (int g = 0; g < ROWS; ++g) t += group[g][c];
-                part[k * d + c] = t;
+                sums[k * d + c] = t;
             }
         }
     };
