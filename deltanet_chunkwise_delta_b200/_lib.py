@@ -8,6 +8,7 @@ or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -55,6 +56,8 @@ def library_path() -> str:
 def load(path: Optional[str] = None):
     """Load the shared library (built in-tree by ``build.py``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -379,59 +382,70 @@ def deltanet_fwd_noalloc(q, k, v, beta, initial_state=None, chunk_size: int = 64
 _DESC = struct.Struct("@Pii8q")
 assert _DESC.size == ctypes.sizeof(DnTensor)
 _PAD = (0, 0, 0, 0)
+_MAX_TENSORS = 16
+
+
+class _Buffers(threading.local):
+    """A thread's room for the descriptors of one call (the library copies what it needs
+    before the call returns)."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(_DESC.size * _MAX_TENSORS)
+        self.base = ctypes.addressof(self.buf)
+
+
+_buffers = _Buffers()
 
 
 def _descriptors(*tensors):
-    """Descriptors of the given tensors (None stays None) in one buffer: (buffer, addresses).
-    The buffer has to outlive the call that gets the addresses."""
-    buf = ctypes.create_string_buffer(_DESC.size * len(tensors))
-    base = ctypes.addressof(buf)
+    """Addresses of the descriptors of the given tensors (None stays None), good until this
+    thread's next call."""
+    b = _buffers
+    buf, base, pack, size = b.buf, b.base, _DESC.pack_into, _DESC.size
     addr, at = [], 0
     for t in tensors:
         if t is None:
             addr.append(None)
             continue
-        dt, n = _DT.get(t.dtype), t.dim()
+        shape = t.shape
+        n = len(shape)
+        dt = _DT.get(t.dtype)
         if dt is None:
             raise TypeError(f"unsupported dtype {t.dtype}")
-        if not 1 <= n <= 4:
+        if n == 4:
+            pack(buf, at, t.data_ptr(), dt, 4, *shape, *t.stride())
+        elif 1 <= n < 4:
+            pad = _PAD[n:]
+            pack(buf, at, t.data_ptr(), dt, n, *shape, *pad, *t.stride(), *pad)
+        else:
             raise ValueError("1 to 4 dimensions")
-        pad = _PAD[n:]
-        _DESC.pack_into(buf, at, t.data_ptr(), dt, n, *t.shape, *pad, *t.stride(), *pad)
         addr.append(base + at)
-        at += _DESC.size
-    return buf, addr
+        at += size
+    return addr
 
 
-class _On:
-    """The device and stream of one call: entering makes them current for the allocations
-    and the launch where they are not, ``handle`` is the stream's handle."""
+_HERE = contextlib.nullcontext()
 
-    def __init__(self, name, stream, lead, *others):
-        if not isinstance(lead, torch.Tensor) or not lead.is_cuda:
-            raise ValueError(f"{name} runs on CUDA tensors only")
-        dev = lead.device
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev)
-        self.handle = _stream_handle(dev, stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
+def _place(name, stream, lead, *others):
+    """The handle of the stream of one call, and a context in which its device and stream are
+    the current ones, for the allocations and the launch."""
+    idx = lead.get_device() if isinstance(lead, torch.Tensor) else -1
+    if idx < 0:
+        raise ValueError(f"{name} runs on CUDA tensors only")
+    for t in others:
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"{name}: tensors on {lead.device} and {t.device}")
+    if stream is not None:
+        if stream.device.index != idx:
+            raise ValueError(f"{name}: tensors on {lead.device}, stream on {stream.device}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    here = _HERE if torch.cuda.current_device() == idx else torch.cuda.device(idx)
+    return torch.cuda.current_stream(idx).cuda_stream, here
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _check(st: int) -> None:
@@ -452,11 +466,11 @@ def deltanet_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch
     state [M, H, d_k, d_v] fp32; slot_idx int32 [N] names each request's row of it (-1: a
     padding request, whose rows of out are zero), None: request n uses row n.  Returns out
     [N, T, H, d_v].  Asynchronous on ``stream`` (default: torch's current stream)."""
-    on = _On("deltanet_step", stream, q, k, v, beta, state, g, slot_idx, out)
-    with on as handle:
+    handle, here = _place("deltanet_step", stream, q, k, v, beta, state, g, slot_idx, out)
+    with here:
         if out is None:
-            out = torch.empty((*q.shape[:3], v.shape[-1]), dtype=q.dtype, device=q.device)
-        keep, a = _descriptors(q, k, v, beta, g, state, slot_idx, out)
+            out = q.new_empty((*q.shape[:3], v.shape[-1]))
+        a = _descriptors(q, k, v, beta, g, state, slot_idx, out)
         _check(load().deltanet_step(*a[:5], int(n_h), *a[5:], handle))
     return out
 
@@ -473,14 +487,14 @@ def deltanet_scan_fwd(x: torch.Tensor, g: torch.Tensor,
     initial_state [N, D] fp32 or None; cu_seqlens int32 [N+1] or None.  Returns (out,
     final_state or None): every h_t in the dtype of x and the last one of each sequence
     in fp32."""
-    on = _On("deltanet_scan_fwd", stream, x, g, initial_state, cu_seqlens, out, final_state)
-    with on as handle:
+    handle, here = _place("deltanet_scan_fwd", stream, x, g, initial_state, cu_seqlens, out, final_state)
+    with here:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _like(x)
         if final_state is None and output_final_state:
             n = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
             final_state = torch.empty((n, x.shape[-1]), dtype=torch.float32, device=x.device)
-        keep, a = _descriptors(x, g, initial_state, cu_seqlens, out, final_state)
+        a = _descriptors(x, g, initial_state, cu_seqlens, out, final_state)
         _check(load().deltanet_scan_fwd(*a, handle))
     return out, final_state
 
@@ -494,16 +508,16 @@ def deltanet_scan_bwd(g: torch.Tensor, out: torch.Tensor, d_out: torch.Tensor,
     """Gradients of ``deltanet_scan_fwd`` from its output ``out``: (d_x, d_g,
     d_initial_state), the last where initial_state (or a buffer for it) is given, else
     None.  d_final_state [N, D] fp32, or None for zeros."""
-    on = _On("deltanet_scan_bwd", stream, g, out, d_out, initial_state, cu_seqlens, d_final_state,
-             d_x, d_g, d_initial_state)
-    with on as handle:
+    handle, here = _place("deltanet_scan_bwd", stream, g, out, d_out, initial_state, cu_seqlens,
+                          d_final_state, d_x, d_g, d_initial_state)
+    with here:
         if d_x is None:
-            d_x = torch.empty(out.shape, dtype=out.dtype, device=g.device)
+            d_x = _like(out)
         if d_g is None:
-            d_g = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+            d_g = _like(g)
         if d_initial_state is None and initial_state is not None:
-            d_initial_state = torch.empty(initial_state.shape, dtype=torch.float32, device=g.device)
-        keep, a = _descriptors(g, out, initial_state, cu_seqlens, d_out, d_final_state, d_x, d_g,
+            d_initial_state = _like(initial_state)
+        a = _descriptors(g, out, initial_state, cu_seqlens, d_out, d_final_state, d_x, d_g,
                                d_initial_state)
         _check(load().deltanet_scan_bwd(*a, handle))
     return d_x, d_g, d_initial_state
@@ -515,11 +529,11 @@ def deltanet_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     """The gated linear recurrence for the few tokens of a decoding step: x, g [N, T, D],
     state [M, D] fp32 updated in place, slot_idx as ``deltanet_step``.  Returns out
     [N, T, D]."""
-    on = _On("deltanet_scan_step", stream, x, g, state, slot_idx, out)
-    with on as handle:
+    handle, here = _place("deltanet_scan_step", stream, x, g, state, slot_idx, out)
+    with here:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        keep, a = _descriptors(x, g, state, slot_idx, out)
+            out = _like(x)
+        a = _descriptors(x, g, state, slot_idx, out)
         _check(load().deltanet_scan_step(*a, handle))
     return out
 
@@ -549,14 +563,14 @@ def deltanet_norm_fwd(y: torch.Tensor, weight: Optional[torch.Tensor] = None,
     residual_out): without residual (y2, None); with it (n, r'), n None without
     next_weight."""
     act = _activation(activation)
-    on = _On("deltanet_norm_fwd", stream, y, weight, gate, residual, scale, next_weight, out,
-             residual_out)
-    with on as handle:
+    handle, here = _place("deltanet_norm_fwd", stream, y, weight, gate, residual, scale, next_weight,
+                          out, residual_out)
+    with here:
         if out is None and (residual is None or next_weight is not None):
-            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            out = _like(y)
         if residual_out is None and residual is not None:
-            residual_out = torch.empty(y.shape, dtype=residual.dtype, device=y.device)
-        keep, a = _descriptors(y, weight, gate, residual, scale, next_weight, out, residual_out)
+            residual_out = _like(residual)
+        a = _descriptors(y, weight, gate, residual, scale, next_weight, out, residual_out)
         _check(load().deltanet_norm_fwd(*a[:3], act, *a[3:6], float(eps), *a[6:], handle))
     return out, residual_out
 
@@ -585,9 +599,9 @@ def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
     where the forward call has no out) and d_residual_out of residual_out (None: zeros,
     where next_weight is given).  Buffers for the row gradients may be passed in."""
     act = _activation(activation)
-    on = _On("deltanet_norm_bwd", stream, y, d_out, weight, gate, residual, scale, next_weight,
-             d_residual_out, d_y, d_gate, d_residual)
-    with on as handle:
+    handle, here = _place("deltanet_norm_bwd", stream, y, d_out, weight, gate, residual, scale,
+                          next_weight, d_residual_out, d_y, d_gate, d_residual)
+    with here:
         dev, lib = y.device, load()
         like = lambda t, given: given if given is not None or t is None else             torch.empty(t.shape, dtype=t.dtype, device=dev)
         d_y, d_gate, d_residual = like(y, d_y), like(gate, d_gate), like(residual, d_residual)
@@ -597,7 +611,7 @@ def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
             sums = [torch.empty(d, dtype=torch.float32, device=dev) if p else None for p in params]
             n = int(lib.deltanet_norm_workspace(y.numel() // d if d else 0, d))
             work = torch.empty(n, dtype=torch.float32, device=dev) if n else None
-        keep, a = _descriptors(y, weight, gate, residual, scale, next_weight, d_out,
+        a = _descriptors(y, weight, gate, residual, scale, next_weight, d_out,
                                d_residual_out, d_y, sums[0], d_gate, d_residual, sums[1], sums[2],
                                work)
         _check(lib.deltanet_norm_bwd(*a[:3], act, *a[3:6], float(eps), *a[6:], handle))

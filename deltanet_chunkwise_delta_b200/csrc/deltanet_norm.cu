@@ -169,7 +169,10 @@ dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t str
         const int64_t grid = need > sms ? std::min<int64_t>(need, norm_resident(kern, TH, smem, sms)) : need;
         kern<<<(unsigned)grid, TH, smem, stream>>>(p);
     });
-    if (!done) k_norm_fwd<Y, R><<<(unsigned)p.rows, kNormThreads, 0, stream>>>(p);
+    if (!done) {
+        auto* kern = wide ? k_norm_fwd_long<Y, R, true> : k_norm_fwd_long<Y, R, false>;
+        kern<<<(unsigned)std::min<int64_t>(p.rows, 4 * sms), kNormLong, 0, stream>>>(p);
+    }
     return ok ? launched(1) : DN_ERR_CUDA;
 }
 
@@ -187,9 +190,12 @@ dn_status norm_bwd_run(const NormParams& p, bool wide, int sms, int& ctas, cudaS
         kern<<<ctas, TH, smem, stream>>>(p);
     });
     if (!done) {
-        auto* kern = k_norm_bwd<Y, R>;
-        const int smem = 3 * p.d * (int)sizeof(float);
-        if ((ok = norm_smem(kern, smem))) kern<<<ctas, kNormThreads, smem, stream>>>(p);
+        auto* kern = wide ? k_norm_bwd_long<Y, R, true> : k_norm_bwd_long<Y, R, false>;
+        const int smem = 3 * ((p.d + kNormLong * 8 - 1) / (kNormLong * 8)) * kNormLong * 8 * (int)sizeof(float);
+        if ((ok = norm_smem(kern, smem))) {
+            ctas = std::min(ctas, norm_resident(kern, kNormLong, smem, sms));
+            kern<<<ctas, kNormLong, smem, stream>>>(p);
+        }
     }
     return ok ? DN_OK : DN_ERR_CUDA;
 }

@@ -83,18 +83,6 @@ __device__ __forceinline__ float norm_act(float z, int act, float* grad = nullpt
     return z * s;
 }
 
-// Sum over the CTA (same order on every thread and every call).
-__device__ __forceinline__ float cta_sum(float x, float* sh) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += sh[w];
-    return s;
-}
-
 // ---- rows that fit a group of threads, 8 elements each -----------------------------------
 //
 // TPR threads hold a row in registers (8, 16 or 32 of a warp, or a whole CTA): every element is
@@ -141,11 +129,21 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                  : "memory");
 }
 
-// A thread's 8 elements of a row.
-template <typename E, int TPR, bool VEC>
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
+// A thread's 8 elements of a row.  VEC: 8 neighbours (all bf16: 16 bytes), or, where fp32 takes
+// part (SPLIT), two times 4 neighbours 4 TPR apart, so that a warp's accesses stay contiguous
+// (8 neighbours of fp32 would move in 16-byte halves of 32-byte pieces: half of each sector
+// per access, 85 -> 70 us for the residual case).  Without VEC: 8 elements TPR apart.
+template <typename E, int TPR, bool VEC, bool SPLIT>
 struct RowPart {
-    static constexpr int kPieces = sizeof(E) / 2;      // of 16 bytes
-    __device__ static __forceinline__ int col(int l, int e) { return VEC ? l * 8 + e : e * TPR + l; }
+    static constexpr int kPieces = sizeof(E) / 2;      // of 16 bytes in shared memory
+    __device__ static __forceinline__ int col(int l, int e) {
+        return !VEC ? e * TPR + l : !SPLIT ? l * 8 + e : (e >> 2) * TPR * 4 + l * 4 + (e & 3);
+    }
     __device__ static __forceinline__ void unpack16(const uint4* q, float* f) {
         if constexpr (sizeof(E) == 2) {
             const uint32_t u[4] = {q->x, q->y, q->z, q->w};
@@ -164,9 +162,23 @@ struct RowPart {
     __device__ static __forceinline__ void load(const E* row, int l, int d, float* f) {
         if constexpr (VEC) {
             uint4 q[kPieces] = {};
-            if (l * 8 < d)
+            if constexpr (!SPLIT) {
+                if (l * 8 < d)
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(row + l * 8) + i);
+                    for (int i = 0; i < kPieces; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(row + l * 8) + i);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (col(l, 4 * h) < d) {
+                        if constexpr (sizeof(E) == 4) {
+                            q[h] = __ldg(reinterpret_cast<const uint4*>(row + col(l, 4 * h)));
+                        } else {
+                            const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + col(l, 4 * h)));
+                            if (h == 0) q[0].x = u.x, q[0].y = u.y;
+                            else q[0].z = u.x, q[0].w = u.y;
+                        }
+                    }
+            }
             unpack16(q, f);
         } else {
 #pragma unroll
@@ -174,17 +186,22 @@ struct RowPart {
         }
     }
     __device__ static __forceinline__ void store(E* row, int l, int d, const float* f) {
-        if constexpr (VEC) {
-            if constexpr (sizeof(E) == 2) {
-                uint32_t u[4];
+        if constexpr (VEC && sizeof(E) == 2) {
+            uint32_t u[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pack(f + 2 * i, u[i]);
-                *reinterpret_cast<uint4*>(row + l * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+            for (int i = 0; i < 4; ++i) pack(f + 2 * i, u[i]);
+            if constexpr (!SPLIT) {
+                if (l * 8 < d) *reinterpret_cast<uint4*>(row + l * 8) = make_uint4(u[0], u[1], u[2], u[3]);
             } else {
-                float4* o = reinterpret_cast<float4*>(row + l * 8);
-                o[0] = make_float4(f[0], f[1], f[2], f[3]);
-                o[1] = make_float4(f[4], f[5], f[6], f[7]);
+                if (col(l, 0) < d) *reinterpret_cast<uint2*>(row + col(l, 0)) = make_uint2(u[0], u[1]);
+                if (col(l, 4) < d) *reinterpret_cast<uint2*>(row + col(l, 4)) = make_uint2(u[2], u[3]);
             }
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (col(l, 4 * h) < d)
+                    *reinterpret_cast<float4*>(row + col(l, 4 * h)) =
+                        make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -192,9 +209,20 @@ struct RowPart {
         }
     }
     // this thread's pieces into shared memory (16 bytes a thread side by side), and from there
-    __device__ static __forceinline__ void fetch(const E* piece, uint4* place) {
+    __device__ static __forceinline__ void fetch(const E* row, int l, int d, uint4* place) {
+        if constexpr (!SPLIT) {
+            if (l * 8 < d)
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) cp_async16(place + i * kNormCta<TPR>, reinterpret_cast<const uint4*>(piece) + i);
+                for (int i = 0; i < kPieces; ++i)
+                    cp_async16(place + i * kNormCta<TPR>, reinterpret_cast<const uint4*>(row + l * 8) + i);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (col(l, 4 * h) < d) {
+                    if constexpr (sizeof(E) == 4) cp_async16(place + h * kNormCta<TPR>, row + col(l, 4 * h));
+                    else cp_async8(reinterpret_cast<uint2*>(place) + h, row + col(l, 4 * h));
+                }
+        }
     }
     __device__ static __forceinline__ void take(const uint4* place, float* f) {
         uint4 q[kPieces];
@@ -205,18 +233,18 @@ struct RowPart {
 };
 
 // 8 of a parameter vector (`none` where it is not given)
-template <int TPR, bool VEC>
+template <int TPR, bool VEC, bool SPLIT>
 __device__ __forceinline__ void param_part(const ParamVec& v, int l, int d, float none, float* f) {
     if (!v.p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = none;
     } else if (VEC && v.vec) {
-        if (v.bf16) RowPart<__nv_bfloat16, TPR, true>::load(static_cast<const __nv_bfloat16*>(v.p), l, d, f);
-        else RowPart<float, TPR, true>::load(static_cast<const float*>(v.p), l, d, f);
+        if (v.bf16) RowPart<__nv_bfloat16, TPR, true, SPLIT>::load(static_cast<const __nv_bfloat16*>(v.p), l, d, f);
+        else RowPart<float, TPR, true, SPLIT>::load(static_cast<const float*>(v.p), l, d, f);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = RowPart<float, TPR, VEC>::col(l, e);
+            const int c = RowPart<float, TPR, VEC, SPLIT>::col(l, e);
             f[e] = c < d ? ld_param(v, c) : 0.f;
         }
     }
@@ -249,21 +277,21 @@ struct NormPlan {
 
 template <typename Y, typename R, int TPR, bool VEC, bool RES, bool SAME>
 __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
-    using PY = RowPart<Y, TPR, VEC>;
-    using PR = RowPart<R, TPR, VEC>;
+    constexpr bool SPLIT = sizeof(Y) == 4 || (RES && sizeof(R) == 4);
+    using PY = RowPart<Y, TPR, VEC, SPLIT>;
+    using PR = RowPart<R, TPR, VEC, SPLIT>;
     using Plan = NormPlan<Y, R, RES, false>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
     extern __shared__ uint4 ring_mem[];                // [2][Plan::all][TH], with VEC
     __shared__ __align__(16) float sh[2][2][32];
     const int l = threadIdx.x % TPR, d = p.d;
-    const bool part = !VEC || l * 8 < d;               // VEC: this thread has elements
     int turn = 0, s = 0;
     const float inv = 1.f / (float)d;
     float w[8], sc[8], nw[8];
-    param_part<TPR, VEC>(p.w, l, d, 1.f, w);
+    param_part<TPR, VEC, SPLIT>(p.w, l, d, 1.f, w);
     if (RES) {
-        param_part<TPR, VEC>(p.sc, l, d, 1.f, sc);
-        param_part<TPR, VEC>(p.nw, l, d, 1.f, nw);
+        param_part<TPR, VEC, SPLIT>(p.sc, l, d, 1.f, sc);
+        param_part<TPR, VEC, SPLIT>(p.nw, l, d, 1.f, nw);
     }
     if (VEC)                                           // what is never fetched reads as zeros
         for (int i = 0; i < 2 * Plan::all; ++i) ring_mem[i * TH + threadIdx.x] = make_uint4(0, 0, 0, 0);
@@ -271,9 +299,9 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
     auto fetch = [&](const RowAt<SAME>& at, bool on, int s) {
         if constexpr (VEC) {
             if (on) {
-                PY::fetch(at.template of<const Y>(p.y) + l * 8, place(s, 0));
-                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate) + l * 8, place(s, Plan::z));
-                if (RES) PR::fetch(at.template of<const R>(p.res) + l * 8, place(s, Plan::r));
+                PY::fetch(at.template of<const Y>(p.y), l, d, place(s, 0));
+                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate), l, d, place(s, Plan::z));
+                if (RES) PR::fetch(at.template of<const R>(p.res), l, d, place(s, Plan::r));
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -281,12 +309,12 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_fwd_rows(NormParams p) {
     const int64_t step = (int64_t)gridDim.x * ROWS;
     int64_t base = (int64_t)blockIdx.x * ROWS, row = base + threadIdx.x / TPR;
     RowAt<SAME> at(p, row < p.rows ? (unsigned)row : 0u);
-    fetch(at, part && row < p.rows, 0);
+    fetch(at, row < p.rows, 0);
     for (; base < p.rows; base += step, s ^= 1) {
-        const bool on = part && row < p.rows;          // what a row past the last computes is not stored
+        const bool on = row < p.rows;                  // what a row past the last computes is not stored
         row += step;
         const RowAt<SAME> next(p, row < p.rows ? (unsigned)row : 0u);
-        fetch(next, part && row < p.rows, s ^ 1);
+        fetch(next, row < p.rows, s ^ 1);
         if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
         float v[8], z[8], r[8];
         if constexpr (VEC) {
@@ -342,21 +370,21 @@ __device__ __forceinline__ void param_take(const float4* mem, int k, float* f) {
 
 template <typename Y, typename R, int TPR, bool VEC, bool RES, bool SAME>
 __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
-    using PY = RowPart<Y, TPR, VEC>;
-    using PR = RowPart<R, TPR, VEC>;
+    constexpr bool SPLIT = sizeof(Y) == 4 || (RES && sizeof(R) == 4);
+    using PY = RowPart<Y, TPR, VEC, SPLIT>;
+    using PR = RowPart<R, TPR, VEC, SPLIT>;
     using Plan = NormPlan<Y, R, RES, true>;
     constexpr int TH = kNormCta<TPR>, ROWS = TH / TPR;
     extern __shared__ uint4 ring_mem[];                // parameters, then [2][Plan::all][TH], with VEC
     __shared__ __align__(16) float sh[2][2][32];
     const int l = threadIdx.x % TPR, d = p.d;
-    const bool part = !VEC || l * 8 < d;
     int turn = 0, s = 0;
     const float inv = 1.f / (float)d;
     float aw[8] = {}, as[8] = {}, an[8] = {};          // sums over this thread's rows
     float4* const par = reinterpret_cast<float4*>(ring_mem);
     auto keep = [&](int k, const ParamVec& v) {
         float f[8];
-        param_part<TPR, VEC>(v, l, d, 1.f, f);
+        param_part<TPR, VEC, SPLIT>(v, l, d, 1.f, f);
         par[(k * 2) * TH + threadIdx.x] = make_float4(f[0], f[1], f[2], f[3]);
         par[(k * 2 + 1) * TH + threadIdx.x] = make_float4(f[4], f[5], f[6], f[7]);
     };
@@ -369,11 +397,11 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
     auto fetch = [&](const RowAt<SAME>& at, bool on, int s) {
         if constexpr (VEC) {
             if (on) {
-                PY::fetch(at.template of<const Y>(p.y) + l * 8, place(s, 0));
-                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate) + l * 8, place(s, Plan::z));
-                if (p.dout.p) PY::fetch(at.template of<const Y>(p.dout) + l * 8, place(s, Plan::dout));
-                if (RES) PR::fetch(at.template of<const R>(p.res) + l * 8, place(s, Plan::r));
-                if (RES && p.drout.p) PR::fetch(at.template of<const R>(p.drout) + l * 8, place(s, Plan::dr));
+                PY::fetch(at.template of<const Y>(p.y), l, d, place(s, 0));
+                if (p.gate.p) PY::fetch(at.template of<const Y>(p.gate), l, d, place(s, Plan::z));
+                if (p.dout.p) PY::fetch(at.template of<const Y>(p.dout), l, d, place(s, Plan::dout));
+                if (RES) PR::fetch(at.template of<const R>(p.res), l, d, place(s, Plan::r));
+                if (RES && p.drout.p) PR::fetch(at.template of<const R>(p.drout), l, d, place(s, Plan::dr));
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -381,14 +409,14 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
     const int64_t step = (int64_t)gridDim.x * ROWS;
     int64_t base = (int64_t)blockIdx.x * ROWS, row = base + threadIdx.x / TPR;
     RowAt<SAME> at(p, row < p.rows ? (unsigned)row : 0u);
-    fetch(at, part && row < p.rows, 0);
+    fetch(at, row < p.rows, 0);
     for (; base < p.rows; base += step, s ^= 1) {
-        const bool is = row < p.rows, on = part && is;
+        const bool on = row < p.rows;
         row += step;
         const RowAt<SAME> next(p, row < p.rows ? (unsigned)row : 0u);
-        fetch(next, part && row < p.rows, s ^ 1);
+        fetch(next, row < p.rows, s ^ 1);
         if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        if (VEC && ROWS > 1 && !is)                    // past the last row: zeros, nothing into the sums
+        if (VEC && ROWS > 1 && !on)                    // past the last row: zeros, nothing into the sums
             for (int i = 0; i < Plan::all; ++i) *place(s, i) = make_uint4(0, 0, 0, 0);
         const int dd = on ? d : 0;
         float y[8], y1[8], a[8], da[8], dv[8], w[8];   // y: y rstd1 from the first sum on
@@ -405,7 +433,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
         if (p.w.p) {
             float q = dot8(y, y);
             row_sum<TPR, 1>(&q, sh, turn);
-            rstd1 = is ? rsqrtf(q * inv + p.eps) : 0.f;
+            rstd1 = on ? rsqrtf(q * inv + p.eps) : 0.f;
             param_take<TPR, VEC>(par, 0, w);
             mul8(y, rstd1, y);
             mul8(y, w, y1);
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
                 mul8(t, dn, t);
                 float v[2] = {dot8(r, r), dot8(t, r)};
                 row_sum<TPR, 2>(v, sh, turn);
-                const float rstd2 = is ? rsqrtf(v[0] * inv + p.eps) : 0.f;
+                const float rstd2 = on ? rsqrtf(v[0] * inv + p.eps) : 0.f;
                 const float m2 = -v[1] * inv * rstd2 * rstd2;
                 fma8(r, m2, t, t);
                 fma8(t, rstd2, dv, dv);
@@ -477,14 +505,14 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
         if constexpr (ROWS == 1) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int c = RowPart<float, TPR, VEC>::col(l, e);
+                const int c = RowPart<float, TPR, VEC, SPLIT>::col(l, e);
                 if (c < d) sums[k * d + c] = acc[e];
             }
         } else {
             __shared__ float group[ROWS][TPR * 8];
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) group[threadIdx.x / TPR][RowPart<float, TPR, VEC>::col(l, e)] = acc[e];
+            for (int e = 0; e < 8; ++e) group[threadIdx.x / TPR][RowPart<float, TPR, VEC, SPLIT>::col(l, e)] = acc[e];
             __syncthreads();
             for (int c = threadIdx.x; c < d; c += TH) {
                 float t = 0.f;
@@ -498,134 +526,232 @@ __global__ void __launch_bounds__(kNormCta<TPR>) k_norm_bwd_rows(NormParams p) {
     if (p.nw.p) put(2, an);
 }
 
-// ---- longer rows: element by element, the row read again for each sum --------------------
+// ---- longer rows: piece by piece, the row read again (from the caches) for each sum ----------
 
-template <typename Y, typename R>
-__global__ void __launch_bounds__(kNormThreads) k_norm_fwd(NormParams p) {
-    __shared__ float sh[kNormThreads / 32];
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const unsigned u = (unsigned)row, i2 = u % p.n2, i1 = u / p.n2 % p.n1, i0 = u / p.n2 / p.n1;
-        const Y* y = row_ptr<const Y>(p.y, i0, i1, i2);
-        const Y* z = p.gate.p ? row_ptr<const Y>(p.gate, i0, i1, i2) : nullptr;
-        const R* r = p.res.p ? row_ptr<const R>(p.res, i0, i1, i2) : nullptr;
-        float rstd1 = 1.f, rstd2 = 1.f;
+constexpr int kNormLong = 512;
+
+// A piece: 8 elements per thread, kNormLong * 8 of the row from `c0` on.
+template <typename Y, typename R, bool VEC>
+struct LongRow {
+    using PY = RowPart<Y, kNormLong, VEC, VEC>;
+    using PR = RowPart<R, kNormLong, VEC, VEC>;
+    const NormParams& p;
+    const Y *y, *z, *dout;
+    const R *r, *drout;
+    __device__ __forceinline__ LongRow(const NormParams& p_, const RowAt<false>& at) : p(p_) {
+        y = at.of<const Y>(p.y);
+        z = p.gate.p ? at.of<const Y>(p.gate) : nullptr;
+        r = p.res.p ? at.of<const R>(p.res) : nullptr;
+        dout = p.dout.p ? at.of<const Y>(p.dout) : nullptr;
+        drout = p.drout.p ? at.of<const R>(p.drout) : nullptr;
+    }
+    __device__ __forceinline__ void param(const ParamVec& v, int c0, float* f) const {
+        ParamVec w = v;
+        if (v.p) w.p = static_cast<const char*>(v.p) + (int64_t)c0 * (v.bf16 ? 2 : 4);
+        param_part<kNormLong, VEC, VEC>(w, threadIdx.x, p.d - c0, 1.f, f);
+    }
+    // y rstd1, y2 (before it y1 in da's factor), act, what dy2 is worth to the gate; r' with a residual
+    __device__ __forceinline__ void chain(int c0, float rstd1, float* yn, float* y2, float* a, float* da, float* rp) const {
+        const int l = threadIdx.x, d = p.d - c0;
+        PY::load(y + c0, l, d, yn);
         if (p.w.p) {
-            float q = 0.f;
-            for (int j = threadIdx.x; j < p.d; j += kNormThreads) {
-                const float v = ld_elem(y + j);
-                q = fmaf(v, v, q);
-            }
-            rstd1 = rsqrtf(cta_sum(q, sh) / p.d + p.eps);
+            float w[8];
+            param(p.w, c0, w);
+            mul8(yn, rstd1, yn);
+            mul8(yn, w, y2);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y2[e] = yn[e];
         }
-        auto chain = [&](int j) {      // y2, or r' with a residual
-            float v = ld_elem(y + j);
-            if (p.w.p) v = v * rstd1 * ld_param(p.w, j);
-            if (z) v *= norm_act(ld_elem(z + j), p.act);
-            if (r) v = ld_elem(r + j) + (p.sc.p ? ld_param(p.sc, j) * v : v);
-            return v;
-        };
+        if (z) {
+            PY::load(z + c0, l, d, a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = norm_act(a[e], p.act, &da[e]);
+            mul8(da, y2, da);
+            mul8(y2, a, y2);
+        }
+        if (r) {
+            float sc[8];
+            param(p.sc, c0, sc);
+            PR::load(r + c0, l, d, rp);
+            fma8(sc, y2, rp, rp);
+        }
+    }
+    __device__ __forceinline__ float rstd_y(float (*sh)[2][32], int& turn) const {
+        if (!p.w.p) return 1.f;
+        float q = 0.f, v[8];
+        for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+            PY::load(y + c0, threadIdx.x, p.d - c0, v);
+            q += dot8(v, v);
+        }
+        row_sum<kNormLong, 1>(&q, sh, turn);
+        return rsqrtf(q / (float)p.d + p.eps);
+    }
+};
+
+template <typename Y, typename R, bool VEC>
+__global__ void __launch_bounds__(kNormLong) k_norm_fwd_long(NormParams p) {
+    __shared__ __align__(16) float sh[2][2][32];
+    int turn = 0;
+    const int l = threadIdx.x;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const RowAt<false> at(p, (unsigned)row);
+        const LongRow<Y, R, VEC> x(p, at);
+        const float rstd1 = x.rstd_y(sh, turn);
+        float yn[8], y2[8], a[8], da[8], rp[8], rstd2 = 0.f;
         if (p.nw.p) {
             float q = 0.f;
-            for (int j = threadIdx.x; j < p.d; j += kNormThreads) {
-                const float v = chain(j);
-                q = fmaf(v, v, q);
+            for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+                x.chain(c0, rstd1, yn, y2, a, da, rp);
+                q += dot8(rp, rp);
             }
-            rstd2 = rsqrtf(cta_sum(q, sh) / p.d + p.eps);
+            row_sum<kNormLong, 1>(&q, sh, turn);
+            rstd2 = rsqrtf(q / (float)p.d + p.eps);
         }
-        Y* out = p.out.p ? row_ptr<Y>(p.out, i0, i1, i2) : nullptr;
-        R* rout = p.rout.p ? row_ptr<R>(p.rout, i0, i1, i2) : nullptr;
-        for (int j = threadIdx.x; j < p.d; j += kNormThreads) {
-            const float v = chain(j);
-            if (rout) st_elem(rout + j, v);
-            if (out) st_elem(out + j, p.nw.p ? v * rstd2 * ld_param(p.nw, j) : v);
+        for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+            x.chain(c0, rstd1, yn, y2, a, da, rp);
+            const int d = p.d - c0;
+            if (!x.r) {
+                LongRow<Y, R, VEC>::PY::store(at.of<Y>(p.out) + c0, l, d, y2);
+                continue;
+            }
+            LongRow<Y, R, VEC>::PR::store(at.of<R>(p.rout) + c0, l, d, rp);
+            if (p.nw.p) {
+                float nw[8];
+                x.param(p.nw, c0, nw);
+                mul8(rp, rstd2, rp);
+                mul8(rp, nw, rp);
+                LongRow<Y, R, VEC>::PY::store(at.of<Y>(p.out) + c0, l, d, rp);
+            }
         }
     }
 }
 
-template <typename Y, typename R>
-__global__ void __launch_bounds__(kNormThreads) k_norm_bwd(NormParams p) {
-    __shared__ float sh[kNormThreads / 32];
-    extern __shared__ float acc[];     // [3][d]: sums for weight, scale, next_weight
-    const int d = p.d;
-    for (int j = threadIdx.x; j < 3 * d; j += kNormThreads) acc[j] = 0.f;
-    __syncthreads();
+template <typename Y, typename R, bool VEC>
+__global__ void __launch_bounds__(kNormLong) k_norm_bwd_long(NormParams p) {
+    using Row = LongRow<Y, R, VEC>;
+    extern __shared__ float4 acc[];        // [3][pieces][2][kNormLong]: sums for weight, scale, next_weight
+    __shared__ __align__(16) float sh[2][2][32];
+    int turn = 0;
+    const int l = threadIdx.x, pieces = (p.d + kNormLong * 8 - 1) / (kNormLong * 8);
+    const float inv = 1.f / (float)p.d;
+    for (int i = 0; i < 3 * pieces * 2; ++i) acc[i * kNormLong + l] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int k, int c0, const float* f) {    // a thread's own sums
+        float4* q = acc + ((k * pieces + c0 / (kNormLong * 8)) * 2) * kNormLong + l;
+        float4 u = q[0], v = q[kNormLong];
+        u = make_float4(u.x + f[0], u.y + f[1], u.z + f[2], u.w + f[3]);
+        v = make_float4(v.x + f[4], v.y + f[5], v.z + f[6], v.w + f[7]);
+        q[0] = u;
+        q[kNormLong] = v;
+    };
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const unsigned u = (unsigned)row, i2 = u % p.n2, i1 = u / p.n2 % p.n1, i0 = u / p.n2 / p.n1;
-        const Y* y = row_ptr<const Y>(p.y, i0, i1, i2);
-        const Y* z = p.gate.p ? row_ptr<const Y>(p.gate, i0, i1, i2) : nullptr;
-        const R* r = p.res.p ? row_ptr<const R>(p.res, i0, i1, i2) : nullptr;
-        const Y* dout = p.dout.p ? row_ptr<const Y>(p.dout, i0, i1, i2) : nullptr;
-        const R* drout = p.drout.p ? row_ptr<const R>(p.drout, i0, i1, i2) : nullptr;
-        float rstd1 = 1.f, rstd2 = 1.f, m2 = 0.f, m1 = 0.f;
-        if (p.w.p) {
-            float q = 0.f;
-            for (int j = threadIdx.x; j < d; j += kNormThreads) {
-                const float v = ld_elem(y + j);
-                q = fmaf(v, v, q);
-            }
-            rstd1 = rsqrtf(cta_sum(q, sh) / d + p.eps);
-        }
-        struct Elem { float y, y1, y2, a, da, r; };
-        auto chain = [&](int j) {
-            Elem e;
-            e.y = ld_elem(y + j);
-            e.y1 = p.w.p ? e.y * rstd1 * ld_param(p.w, j) : e.y;
-            e.a = 1.f;
-            e.da = 0.f;
-            if (z) e.a = norm_act(ld_elem(z + j), p.act, &e.da);
-            e.y2 = e.y1 * e.a;
-            e.r = r ? ld_elem(r + j) + (p.sc.p ? ld_param(p.sc, j) * e.y2 : e.y2) : 0.f;
-            return e;
-        };
+        const RowAt<false> at(p, (unsigned)row);
+        const Row x(p, at);
+        const float rstd1 = x.rstd_y(sh, turn);
+        float yn[8], y2[8], a[8], da[8], rp[8], dn[8], t[8], dv[8];
+        float rstd2 = 0.f, m2 = 0.f, m1 = 0.f;
         if (p.nw.p) {
-            float q = 0.f, c = 0.f;
-            for (int j = threadIdx.x; j < d; j += kNormThreads) {
-                const Elem e = chain(j);
-                q = fmaf(e.r, e.r, q);
-                c = fmaf(ld_elem(dout + j) * ld_param(p.nw, j), e.r, c);
+            float v[2] = {0.f, 0.f};
+            for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+                x.chain(c0, rstd1, yn, y2, a, da, rp);
+                Row::PY::load(x.dout + c0, l, p.d - c0, dn);
+                x.param(p.nw, c0, t);
+                mul8(t, dn, t);
+                v[0] += dot8(rp, rp);
+                v[1] += dot8(t, rp);
             }
-            rstd2 = rsqrtf(cta_sum(q, sh) / d + p.eps);
-            m2 = cta_sum(c, sh) / d * rstd2 * rstd2;
+            row_sum<kNormLong, 2>(v, sh, turn);
+            rstd2 = rsqrtf(v[0] * inv + p.eps);
+            m2 = -v[1] * inv * rstd2 * rstd2;
         }
-        // gradient of y2 before the residual scale (of r' with a residual)
-        auto top = [&](int j, const Elem& e) {
-            if (!r) return ld_elem(dout + j);
-            float dr = drout ? ld_elem(drout + j) : 0.f;
-            if (p.nw.p) dr += rstd2 * (ld_elem(dout + j) * ld_param(p.nw, j) - e.r * m2);
-            return dr;
+        // dv: the gradient of r' (of y2 without a residual); leaves r' rstd2 in rp
+        auto top = [&](int c0) {
+            const int d = p.d - c0;
+            if (!x.r) {
+                Row::PY::load(x.dout + c0, l, d, dv);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dv[e] = 0.f;
+            if (x.drout) Row::PR::load(x.drout + c0, l, d, dv);
+            if (p.nw.p) {
+                Row::PY::load(x.dout + c0, l, d, dn);
+                x.param(p.nw, c0, t);
+                mul8(t, dn, t);
+                fma8(rp, m2, t, t);
+                fma8(t, rstd2, dv, dv);
+                mul8(rp, rstd2, rp);
+            }
         };
+        // dv from there to the gradient of y1, times weight
+        auto down = [&](int c0, float* w) {
+            if (p.sc.p) {
+                x.param(p.sc, c0, w);
+                mul8(dv, w, dv);
+            }
+            if (x.z) mul8(dv, a, dv);
+            if (p.w.p) x.param(p.w, c0, w);
+        };
+        float w[8];
         if (p.w.p) {
             float c = 0.f;
-            for (int j = threadIdx.x; j < d; j += kNormThreads) {
-                const Elem e = chain(j);
-                float dv = top(j, e);
-                if (p.sc.p) dv *= ld_param(p.sc, j);
-                c = fmaf(dv * e.a * ld_param(p.w, j), e.y, c);
+            for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+                x.chain(c0, rstd1, yn, y2, a, da, rp);
+                top(c0);
+                down(c0, w);
+                mul8(dv, w, dv);
+                c += dot8(dv, yn);
             }
-            m1 = cta_sum(c, sh) / d * rstd1 * rstd1;
+            row_sum<kNormLong, 1>(&c, sh, turn);
+            m1 = -c * inv;
         }
-        for (int j = threadIdx.x; j < d; j += kNormThreads) {
-            const Elem e = chain(j);
-            float dv = top(j, e);
-            if (p.nw.p) acc[2 * d + j] += ld_elem(dout + j) * e.r * rstd2;
-            if (r) st_elem(row_ptr<R>(p.dres, i0, i1, i2) + j, dv);
+        for (int c0 = 0; c0 < p.d; c0 += kNormLong * 8) {
+            const int d = p.d - c0;
+            x.chain(c0, rstd1, yn, y2, a, da, rp);
+            top(c0);
+            if (p.nw.p) {
+                mul8(dn, rp, dn);
+                add(2, c0, dn);
+            }
+            if (x.r) Row::PR::store(at.of<R>(p.dres) + c0, l, d, dv);
             if (p.sc.p) {
-                acc[d + j] += dv * e.y2;
-                dv *= ld_param(p.sc, j);
+                mul8(y2, dv, y2);
+                add(1, c0, y2);
             }
-            if (z) st_elem(row_ptr<Y>(p.dgate, i0, i1, i2) + j, dv * e.y1 * e.da);
-            dv *= e.a;
+            if (x.z) {
+                float dz[8];
+                if (p.sc.p) {
+                    x.param(p.sc, c0, w);
+                    mul8(w, dv, dz);
+                    mul8(dz, da, dz);
+                } else {
+                    mul8(dv, da, dz);
+                }
+                Row::PY::store(at.of<Y>(p.dgate) + c0, l, d, dz);
+            }
+            down(c0, w);
             if (p.w.p) {
-                acc[j] += dv * e.y * rstd1;
-                dv = rstd1 * (dv * ld_param(p.w, j) - e.y * m1);
+                mul8(dv, yn, t);
+                add(0, c0, t);
+                mul8(dv, w, dv);
+                fma8(yn, m1, dv, dv);
+                mul8(dv, rstd1, dv);
             }
-            st_elem(row_ptr<Y>(p.dy, i0, i1, i2) + j, dv);
+            Row::PY::store(at.of<Y>(p.dy) + c0, l, d, dv);
         }
     }
     if (!p.part) return;
-    __syncthreads();
-    float* part = p.part + (int64_t)blockIdx.x * 3 * d;
-    for (int j = threadIdx.x; j < 3 * d; j += kNormThreads) part[j] = acc[j];
+    float* sums = p.part + (int64_t)blockIdx.x * 3 * p.d;
+    for (int k = 0; k < 3; ++k)
+        for (int i = 0; i < pieces; ++i) {
+            const float4 u = acc[((k * pieces + i) * 2) * kNormLong + l], v = acc[((k * pieces + i) * 2 + 1) * kNormLong + l];
+            const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = i * kNormLong * 8 + RowPart<float, kNormLong, VEC, VEC>::col(l, e);
+                if (c < p.d) sums[k * p.d + c] = f[e];
+            }
+        }
 }
 
 // d_weight, d_scale, d_next_weight from the partial sums of G CTAs: 32 columns per CTA, 8

@@ -212,7 +212,7 @@ def test_descriptor_bytes_are_the_struct():
     """The packed descriptors hold what the ctypes structure holds."""
     t = torch.zeros(3, 4, 10)[:, :, 2:7]
     u = torch.zeros(6, dtype=torch.int32)
-    buf, addr = L._descriptors(t, None, u)
+    addr = L._descriptors(t, None, u)
     assert addr[1] is None
     for a, x in ((addr[0], t), (addr[2], u)):
         d, e = L.DnTensor.from_address(a), L.describe(x)
