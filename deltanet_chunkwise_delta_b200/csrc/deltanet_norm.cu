@@ -123,11 +123,19 @@ bool norm_wide(const NormParams& p, int ysize, int rsize) {
     return w;
 }
 
+// Every tensor itself does.
+int norm_line(const NormParams& p) {
+    const RowRef* refs[] = {&p.y, &p.gate, &p.res, &p.dout, &p.drout};
+    for (const RowRef* r : refs)
+        if (r->p && !aligned16(r->p)) return 0;
+    return 1;
+}
+
 // Threads of a row by its length: f(integral_constant<TPR>, bool_constant<VEC>,
 // bool_constant<SAME>); false past the longest row that is held in registers.
 template <int TPR, bool VEC, bool SAME, typename F>
 bool norm_try(int d, F& f) {
-    if (d > TPR * 8) return false;
+    if (d > (TPR <= 1 ? kNormCta<TPR> : TPR) * 8) return false;
     f(std::integral_constant<int, TPR>(), std::bool_constant<VEC>(), std::bool_constant<SAME>());
     return true;
 }
@@ -139,7 +147,7 @@ bool norm_by_length(int d, F& f) {
 template <typename F>
 bool norm_by_length(const NormParams& p, bool wide, F f) {
     if (wide) return norm_same(p) ? norm_by_length<true>(p.d, f) : norm_by_length<false>(p.d, f);
-    return norm_try<32, false, false>(p.d, f) || norm_try<128, false, false>(p.d, f) || norm_try<512, false, false>(p.d, f);
+    return norm_try<32, false, false>(p.d, f) || norm_try<0, false, false>(p.d, f) || norm_try<1, false, false>(p.d, f);
 }
 
 template <typename Kern>
@@ -160,10 +168,13 @@ template <typename Y, typename R, bool RES>
 dn_status norm_fwd_run(const NormParams& p, bool wide, int sms, cudaStream_t stream) {
     bool ok = true;
     const bool done = norm_by_length(p, wide, [&](auto tpr, auto vec, auto same) {
-        constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
+        constexpr int TPR = decltype(tpr)::value, CTA = kNormCta<TPR>, ROWS = TPR <= 1 ? 1 : CTA / TPR;
+        const int TH = TPR <= 1 ? (p.d + 255) / 256 * 32 : CTA;
         constexpr bool VEC = decltype(vec)::value;
         const int64_t need = (p.rows + ROWS - 1) / ROWS;
-        constexpr int smem = VEC ? 2 * NormPlan<Y, R, RES, false>::all * TH * 16 : 0;
+        // without 16-byte rows: two places for the lines of a row of each operand
+        const int smem = VEC ? 2 * NormPlan<Y, R, RES, false>::all * CTA * 16
+                       : p.line ? 2 * ROWS * 16 * (2 * line_pieces<Y>(p.d) + (RES ? line_pieces<R>(p.d) : 0)) : 0;
         auto* kern = k_norm_fwd_rows<Y, R, TPR, VEC, RES, decltype(same)::value>;
         if (!(ok = norm_smem(kern, smem))) return;
         const int64_t grid = need > sms ? std::min<int64_t>(need, norm_resident(kern, TH, smem, sms)) : need;
@@ -180,9 +191,12 @@ template <typename Y, typename R, bool RES>
 dn_status norm_bwd_run(const NormParams& p, bool wide, int sms, int& ctas, cudaStream_t stream) {
     bool ok = true;
     const bool done = norm_by_length(p, wide, [&](auto tpr, auto vec, auto same) {
-        constexpr int TPR = decltype(tpr)::value, TH = kNormCta<TPR>, ROWS = TH / TPR;
+        constexpr int TPR = decltype(tpr)::value, CTA = kNormCta<TPR>, ROWS = TPR <= 1 ? 1 : CTA / TPR;
+        const int TH = TPR <= 1 ? (p.d + 255) / 256 * 32 : CTA;
         constexpr bool VEC = decltype(vec)::value;
-        constexpr int smem = ((VEC ? 2 * NormPlan<Y, R, RES, true>::all : 0) + (RES ? 6 : 2)) * TH * 16;
+        const int smem = (RES ? 6 : 2) * CTA * 16 +
+                         (VEC ? 2 * NormPlan<Y, R, RES, true>::all * CTA * 16
+                              : p.line ? 2 * ROWS * 16 * (3 * line_pieces<Y>(p.d) + (RES ? 2 * line_pieces<R>(p.d) : 0)) : 0);
         auto* kern = k_norm_bwd_rows<Y, R, TPR, VEC, RES, decltype(same)::value>;
         if (!(ok = norm_smem(kern, smem))) return;
         ctas = (int)std::min<int64_t>(ctas, (p.rows + ROWS - 1) / ROWS);
@@ -236,6 +250,7 @@ dn_status deltanet_norm_fwd(const dn_tensor* y, const dn_tensor* weight, const d
     cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
     norm_collapse(p);
+    p.line = norm_line(p);
     return norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
         return norm_fwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, stream);
     });
@@ -294,6 +309,7 @@ dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const d
     if (p.rows > 0) {
         const bool wide = norm_wide(p, (int)elem_size(y->dtype), residual ? (int)elem_size(residual->dtype) : 4);
         norm_collapse(p);
+        p.line = norm_line(p);
         st = norm_by_case(y, residual, [&](auto yt, auto rt, auto has) {
             return norm_bwd_run<decltype(yt), decltype(rt), decltype(has)::value>(p, wide, sms, ctas, stream);
         });
