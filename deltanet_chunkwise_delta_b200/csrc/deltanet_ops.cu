@@ -23,11 +23,17 @@ bool scalars_ok(const dn_tensor* t, const int64_t* dims) {
     return numel(t) == 0 || (t->data && reinterpret_cast<uintptr_t>(t->data) % 4 == 0);
 }
 
+template <typename E, int DK, int DV, bool ONE>
+void launch_step(const StepParams& p, int gate, unsigned grid, cudaStream_t s) {
+    if (gate == 0) k_step<E, DK, DV, 0, ONE><<<grid, DK, 0, s>>>(p);
+    else if (gate == 1) k_step<E, DK, DV, 1, ONE><<<grid, DK, 0, s>>>(p);
+    else k_step<E, DK, DV, 2, ONE><<<grid, DK, 0, s>>>(p);
+}
+
 template <typename E, int DK, int DV>
 void launch_step(const StepParams& p, int gate, unsigned grid, cudaStream_t s) {
-    if (gate == 0) k_step<E, DK, DV, 0><<<grid, kStepThreads, 0, s>>>(p);
-    else if (gate == 1) k_step<E, DK, DV, 1><<<grid, kStepThreads, 0, s>>>(p);
-    else k_step<E, DK, DV, 2><<<grid, kStepThreads, 0, s>>>(p);
+    if (p.T == 1 && p.nh == 1) launch_step<E, DK, DV, true>(p, gate, grid, s);
+    else launch_step<E, DK, DV, false>(p, gate, grid, s);
 }
 
 template <typename E>
@@ -337,9 +343,15 @@ dn_status deltanet_scan_step(const dn_tensor* x, const dn_tensor* g, dn_tensor* 
         p.slots = static_cast<const int*>(slot_idx->data);
         if ((st = dn_stream_flag(dev, stream, &p.err)) != DN_OK) return st;
     }
-    const unsigned grid = (unsigned)(N * ((D + kScanThreads - 1) / kScanThreads));
+    auto fours = [](const void* q, int64_t sn, int64_t st, int32_t dt) {
+        return reinterpret_cast<uintptr_t>(q) % (4 * elem_size(dt)) == 0 && sn % 4 == 0 && st % 4 == 0;
+    };
+    const int V = D % 4 == 0 && fours(p.x, p.x_sn, p.x_st, x->dtype) && fours(p.g, p.g_sn, p.g_st, g->dtype) &&
+                  fours(p.y, p.y_sn, p.y_st, x->dtype) && fours(p.state, p.s_sm, 0, DN_F32) ? 4 : 1;
+    const unsigned grid = (unsigned)(N * ((D + kScanThreads * V - 1) / (kScanThreads * V)));
     by_types(x->dtype, g->dtype, [&](auto xt, auto gt) {
-        k_scan_step<decltype(xt), decltype(gt)><<<grid, kScanThreads, 0, stream>>>(p);
+        if (V == 4) k_scan_step<decltype(xt), decltype(gt), 4><<<grid, kScanThreads, 0, stream>>>(p);
+        else k_scan_step<decltype(xt), decltype(gt), 1><<<grid, kScanThreads, 0, stream>>>(p);
     });
     return launched(1);
 }

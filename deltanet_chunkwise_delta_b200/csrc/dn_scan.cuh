@@ -984,26 +984,39 @@ struct ScanStepParams {
     int N, T, D;
 };
 
-// One thread per (request, channel).
-template <typename X, typename G>
+// One thread per V channels of a request, V = 4 where rows are made of such pieces.
+template <typename X, typename G, int V>
 __global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanStepParams p) {
-    const int per = (p.D + kScanThreads - 1) / kScanThreads;
-    const int n = blockIdx.x / per, c = (blockIdx.x % per) * kScanThreads + threadIdx.x;
+    const int per = (p.D + kScanThreads * V - 1) / (kScanThreads * V);
+    const int n = blockIdx.x / per, c = ((blockIdx.x % per) * kScanThreads + threadIdx.x) * V;
     const int64_t slot = step_slot(p.slots, p.M, n, p.err);
     if (c >= p.D) return;
+    auto load = [](const auto* q, float* f) {
+        if constexpr (V == 4) *reinterpret_cast<float4*>(f) = ld_elem4(q);
+        else f[0] = ld_elem(q);
+    };
+    auto store = [](auto* q, const float* f) {
+        if constexpr (V == 4) st_elem4(q, make_float4(f[0], f[1], f[2], f[3]));
+        else st_elem(q, f[0]);
+    };
     X* y = static_cast<X*>(p.y) + n * p.y_sn + c;
+    alignas(16) float h[V] = {}, xv[V], a[V];
     if (slot < 0) {
-        for (int t = 0; t < p.T; ++t) st_elem(y + t * p.y_st, 0.f);
+        for (int t = 0; t < p.T; ++t) store(y + t * p.y_st, h);
         return;
     }
     const X* x = static_cast<const X*>(p.x) + n * p.x_sn + c;
     const G* g = static_cast<const G*>(p.g) + n * p.g_sn + c;
-    float h = p.state[slot * p.s_sm + c];
+    float* s = p.state + slot * p.s_sm + c;
+    load(s, h);
     for (int t = 0; t < p.T; ++t) {
-        h = fmaf(expf(ld_elem(g + t * p.g_st)), h, ld_elem(x + t * p.x_st));
-        st_elem(y + t * p.y_st, h);
+        load(x + t * p.x_st, xv);
+        load(g + t * p.g_st, a);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(expf(a[v]), h[v], xv[v]);
+        store(y + t * p.y_st, h);
     }
-    p.state[slot * p.s_sm + c] = h;
+    store(s, h);
 }
 
 }  // namespace dn
