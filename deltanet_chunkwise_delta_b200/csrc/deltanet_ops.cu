@@ -105,12 +105,16 @@ bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
            ok(p.y, p.y_sb, p.y_st, x) && (!bwd || (ok(p.h, p.h_sb, p.h_st, x) && ok(p.dg, p.dg_sb, p.dg_st, g)));
 }
 
-// CTAs per cluster: about one and a half CTAs on every SM, while each has tokens.  A cluster
-// costs a start and an exchange per tile, idle SMs cost more: 64 channel tiles of 8192 tokens
-// take 108, 72, 61 and 67 us with 1, 2, 4 and 8; 256 of 2048 tokens 52, 60, 68 and 90 us.
+// CTAs per cluster: enough for most SMs, and on to one and a third of them where a row is
+// split anyway (a cluster's CTAs often sit two to an SM), each with two tiles or more, four in
+// large clusters, whose start and exchange cost more.  Measured with 1, 2, 4, 8, 16: 32
+// channel tiles of 16384 tokens 207, 122, 67, 64, 89 us; 16 of 32768 414, 238, 126, 112, 105
+// us; 256 of 2048 52, 59, 67, 88, 136 us; 128 of 256 6.3, 7.6, 10.5, 20, 49 us.
 int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
     int K = 1;
-    while (K < kScanMaxCluster && items * K < sms + sms / 2 && (int64_t)K * tokens < T) K *= 2;
+    while (K < kScanMaxCluster && (items * K < sms * 7 / 8 || (K > 1 && items * K < sms * 4 / 3)) &&
+           (int64_t)K * tokens * (K < 4 ? 4 : 8) <= T)
+        K *= 2;
     return K;
 }
 
@@ -128,12 +132,13 @@ dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, c
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = K > 1 ? 1 : 0;
-    if (smem > 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return DN_ERR_CUDA;
+    if (K > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DN_ERR_CUDA;
     return cudaLaunchKernelEx(&cfg, kern, p, K, a...) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
 }
 
-constexpr int kScanTs = 8;         // tokens of a warp's run (one channel a lane)
 constexpr int kScanSerialT = 32;   // up to so many tokens, one thread walks a channel
 
 // 16-byte copies: bit 0 for x, 1 for g, 2 for h.
@@ -146,25 +151,20 @@ int scan_wide(const ScanParams& p, int32_t x, int32_t g) {
            (p.h && ok(p.h, p.h_sb, p.h_st, x) ? 4 : 0);
 }
 
-template <typename X, typename G, int V, bool PACKED, bool BWD>
+template <typename X, typename G, bool PACKED, bool BWD, bool EVEN>
 dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
-    const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 32 * V - 1) / (32 * V));
-    if constexpr (V == 2) {
-        // tokens of a warp's run: as many as leave room for two CTAs on an SM
-        constexpr int TS = sizeof(X) == 4 ? 4 : sizeof(G) == 2 && !BWD ? 16 : 8;
-        constexpr int smem = (int)sizeof(ScanStage<X, G, TS, BWD>);
-        const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
-        const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
-        if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-        auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stream, p, wide); };
-        if constexpr (BWD) return K > 1 ? go(k_scan_bwd_piped<X, G, TS, PACKED, true>) : go(k_scan_bwd_piped<X, G, TS, PACKED, false>);
-        else return K > 1 ? go(k_scan_piped<X, G, TS, PACKED, true>) : go(k_scan_piped<X, G, TS, PACKED, false>);
-    } else {
-        const int K = scan_cluster(items, p.T, kScanWarps * kScanTs, sms);
-        if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-        if constexpr (BWD) return scan_launch(k_scan_bwd_tiled<X, G, V, kScanTs, PACKED>, items, K, kScanThreads, 0, stream, p);
-        else return scan_launch(k_scan_tiled<X, G, V, kScanTs, PACKED>, items, K, kScanThreads, 0, stream, p);
-    }
+    const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 63) / 64);
+    // tokens of a warp's run: as many as leave room for two CTAs on an SM
+    constexpr int TS = sizeof(X) == 4 ? 4 : sizeof(G) == 2 && !BWD ? 16 : 8;
+    constexpr int stage = (int)sizeof(ScanStage<X, G, TS, BWD>);
+    static_assert(2 * (stage + 8192 + sizeof(ScanRuns) + 1024) <= 228 * 1024, "two CTAs on an SM, clusters of 8");
+    const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
+    const int smem = stage + (K > 1 ? K * 1024 : 0);
+    const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
+    if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
+    auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stream, p, wide); };
+    if constexpr (BWD) return K > 1 ? go(k_scan_bwd_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_bwd_piped<X, G, TS, PACKED, false, EVEN>);
+    else return K > 1 ? go(k_scan_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_piped<X, G, TS, PACKED, false, EVEN>);
 }
 
 template <bool BWD>
@@ -180,9 +180,9 @@ dn_status scan_run(const ScanParams& p, int32_t x, int32_t g, cudaStream_t strea
             if constexpr (BWD) k_scan_bwd_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
             else k_scan_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
         } else if (scan_pairs(p, x, g, BWD)) {
-            st = p.cu ? scan_tiled<X, G, 2, true, BWD>(p, sms, stream) : scan_tiled<X, G, 2, false, BWD>(p, sms, stream);
+            st = p.cu ? scan_tiled<X, G, true, BWD, true>(p, sms, stream) : scan_tiled<X, G, false, BWD, true>(p, sms, stream);
         } else {
-            st = p.cu ? scan_tiled<X, G, 1, true, BWD>(p, sms, stream) : scan_tiled<X, G, 1, false, BWD>(p, sms, stream);
+            st = p.cu ? scan_tiled<X, G, true, BWD, false>(p, sms, stream) : scan_tiled<X, G, false, BWD, false>(p, sms, stream);
         }
     });
     return st == DN_OK ? launched(1) : st;

@@ -91,19 +91,28 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd_serial(ScanParams p) 
 
 // ---- runs of tokens across warps and CTAs ------------------------------------------------
 //
-// A cluster of K CTAs takes 32 V channels of one batch row (or of the packed tokens) and
-// walks the tokens in tiles of K * 8 * TS, each warp TS tokens of a tile.  A run of tokens
-// maps the h before it to A h + H; a warp forms its run's (A, H) with the tokens in
-// registers, warps exchange theirs through shared memory and CTAs through distributed
-// shared memory, and each then knows the h before its run and finishes its tokens.  Every
+// A cluster of K CTAs takes 64 channels of one batch row (or of the packed tokens), two per
+// lane, and walks the tokens in tiles of K * 8 * TS, each warp TS tokens of a tile.  A run of
+// tokens maps the h before it to A h + H; a warp forms its run's (A, H), warps and CTAs
+// exchange theirs, and each then knows the h before its run and finishes its tokens.  Every
 // element is read once and written once.  Backward walks the tokens from the last one, with
 // c = a_t delta_t (what reaches token t - 1) in the place of h.
 //
 // Packed input: the run's map is cut where a sequence starts (backward: ends).  Such a run
 // passes H on whatever comes in, so that nothing of another sequence, NaN included, leaks:
 // A = -1 marks it (products of decays are >= 0).
-constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanMaxCluster = 8;
+//
+// The tokens come through shared memory (cp.async; a warp reads only what it copied itself).
+// Eight warps form the (A, H) of tile i + 1 before they finish tile i; a ninth joins the
+// warps' runs, sends the CTA's to the cluster's other CTAs (st.async on their mbarriers),
+// waits for theirs and hands every warp the h before its run, all of it behind the finishing
+// of the tile before.  A tile is finished by running its recurrence again from the h that
+// comes in (the decays of an fp32 gate are left in its place in shared memory by the first
+// pass; of a bf16 gate the power is taken twice).  What bounds it: on long inputs the bytes
+// (89 % of the copy rate backward on 65536 x 2048), on bf16 gates the instructions and the
+// exchange per tile (64 % forward on packed 222459 x 2048).
+constexpr int kScanWarps = 8;
+constexpr int kScanMaxCluster = 16;
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -116,13 +125,6 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Stores x at the address of `p` (this CTA's shared memory) in the CTA of rank r.
-__device__ __forceinline__ void st_cluster(float* p, unsigned r, float x) {
-    uint32_t a = (uint32_t)__cvta_generic_to_shared(p), b;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(r));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(b), "f"(x) : "memory");
-}
-
 // carry <- A carry + H (H alone where A is the mark)
 template <bool PACKED>
 __device__ __forceinline__ float run_map(float A, float H, float carry) {
@@ -134,68 +136,6 @@ template <bool PACKED>
 __device__ __forceinline__ float run_prod(float A, float B) {
     const float x = fminf(A * B, 3.402823466e38f);
     return PACKED && (A < 0.f || B < 0.f) ? -1.f : x;
-}
-
-template <int V>
-struct ScanSmem {
-    float warp[2][kScanWarps][2][32 * V];       // (A, H) of each warp's run, by tile parity
-    float cta[2][kScanMaxCluster][2][32 * V];   // (A, H) of each CTA's run
-};
-
-// Exchanges the warps' runs (A, H) of one tile: cin becomes what comes into this warp's run,
-// carry what leaves the tile.  Every thread of the cluster calls it; `before_wait` runs while
-// the other CTAs' runs are on their way.
-template <int V, bool PACKED, typename F>
-__device__ __forceinline__ void scan_exchange(ScanSmem<V>& sm, int par, int K, unsigned rank, const float* A,
-                                              const float* H, float* carry, float* cin, F before_wait) {
-    const int w = threadIdx.x >> 5, l = (threadIdx.x & 31) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sm.warp[par][w][0][l + v] = A[v];
-        sm.warp[par][w][1][l + v] = H[v];
-    }
-    __syncthreads();
-    if (K == 1) {
-        before_wait();
-#pragma unroll
-        for (int i = 0; i < kScanWarps; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (i == w) cin[v] = carry[v];
-                carry[v] = run_map<PACKED>(sm.warp[par][i][0][l + v], sm.warp[par][i][1][l + v], carry[v]);
-            }
-        return;
-    }
-    // the run of the warps before this one, and of the whole CTA (last warp), which goes to every CTA
-    float PA[V], PH[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        PA[v] = 1.f;
-        PH[v] = 0.f;
-        for (int i = 0; i < w; ++i) {
-            const float a = sm.warp[par][i][0][l + v], h = sm.warp[par][i][1][l + v];
-            PH[v] = run_map<PACKED>(a, h, PH[v]);
-            PA[v] = run_prod<PACKED>(a, PA[v]);
-        }
-        if (w == kScanWarps - 1) {
-            const float a = run_prod<PACKED>(A[v], PA[v]), h = run_map<PACKED>(A[v], H[v], PH[v]);
-            for (int r = 0; r < K; ++r) {
-                st_cluster(&sm.cta[par][rank][0][l + v], r, a);
-                st_cluster(&sm.cta[par][rank][1][l + v], r, h);
-            }
-        }
-    }
-    cluster_arrive();
-    before_wait();
-    cluster_wait();
-    for (int r = 0; r < K; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (r == (int)rank) cin[v] = carry[v];
-            carry[v] = run_map<PACKED>(sm.cta[par][r][0][l + v], sm.cta[par][r][1][l + v], carry[v]);
-        }
-#pragma unroll
-    for (int v = 0; v < V; ++v) cin[v] = run_map<PACKED>(PA[v], PH[v], cin[v]);
 }
 
 // The last n with cu[n] <= t, in 0 .. N - 1 whatever cu holds.
@@ -210,244 +150,19 @@ __device__ __forceinline__ int scan_owner(const int* cu, int N, int t) {
 }
 
 // Packed input: state rows of sequences without tokens (forward: final = initial state;
-// backward: d_initial = d_final), channel tile by channel tile.
-template <int V>
+// backward: d_initial = d_final).
 __device__ __forceinline__ void scan_empty(const ScanParams& p, const float* src, int64_t src_sn, int c, int K,
                                            unsigned rank) {
     if (!p.fin) return;
     for (int n = rank * kScanWarps + (threadIdx.x >> 5); n < p.N; n += K * kScanWarps)
-        if (p.cu[n] >= p.cu[n + 1] && c < p.D)
+        if (p.cu[n] >= p.cu[n + 1])
 #pragma unroll
-            for (int v = 0; v < V; ++v) p.fin[n * p.fin_sn + c + v] = src ? src[n * src_sn + c + v] : 0.f;
+            for (int v = 0; v < 2; ++v)
+                if (c + v < p.D) p.fin[n * p.fin_sn + c + v] = src ? src[n * src_sn + c + v] : 0.f;
 }
 
-template <typename X, typename G, int V, int TS, bool PACKED>
-__global__ void __launch_bounds__(kScanThreads, 2) k_scan_tiled(ScanParams p, int K) {
-    __shared__ ScanSmem<V> sm;
-    const unsigned rank = K > 1 ? cluster_rank() : 0;
-    const int item = blockIdx.x / K, ct = (p.D + 32 * V - 1) / (32 * V);
-    const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = (item % ct) * 32 * V + lane * V;
-    const bool live = c < p.D;
-    const X* x = static_cast<const X*>(p.x) + b * p.x_sb + c;
-    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + c;
-    X* y = static_cast<X*>(p.y) + b * p.y_sb + c;
-    if (PACKED) {
-        scan_check_cu(p);
-        scan_empty<V>(p, p.s0, p.s0_sn, c, K, rank);
-    }
-    float carry[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = !PACKED && live && p.s0 ? p.s0[b * p.s0_sn + c + v] : 0.f;
-
-    typename RawVec<X, V>::T rx[TS];
-    typename RawVec<G, V>::T rg[TS];
-    const int step = K * kScanWarps * TS;
-    int64_t t0 = ((int64_t)rank * kScanWarps + w) * TS;      // this warp's first token of the tile
-    auto load = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            const bool in = live && t + j < p.T;
-            rx[j] = in ? ld_raw<X, V>(x + (t + j) * p.x_st) : typename RawVec<X, V>::T{};
-            rg[j] = in ? ld_raw<G, V>(g + (t + j) * p.g_st) : typename RawVec<G, V>::T{};
-        }
-    };
-    load(t0);
-    if (K > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    int par = 0;
-    for (int64_t tile = 0; tile < p.T; tile += step, t0 += step, par ^= 1) {
-        unsigned starts = 0, ends = 0;
-        int owner = 0;
-        if (PACKED) {
-            const int t = (int)(t0 + (lane < TS ? lane : 0) < p.T ? t0 + (lane < TS ? lane : 0) : p.T - 1);
-            owner = scan_owner(p.cu, p.N, t);
-            const bool in = lane < TS && t0 + lane < p.T;
-            starts = __ballot_sync(~0u, in && p.cu[owner] == t);
-            ends = __ballot_sync(~0u, in && p.cu[owner + 1] == t + 1);
-        }
-        float hl[TS][V], Ap[TS][V], A[V], h[V];
-        bool cut = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.f, h[v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            float xv[V], gv[V];
-            unpack(rx[j], xv);
-            unpack(rg[j], gv);
-            if (PACKED && (starts >> j & 1)) {
-                cut = true;
-                const int n = __shfl_sync(~0u, owner, j);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float s = live && p.s0 ? p.s0[n * p.s0_sn + c + v] : 0.f;
-                    h[v] = fmaf(expf(gv[v]), s, xv[v]);
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float a = expf(gv[v]);
-                    h[v] = fmaf(a, h[v], xv[v]);
-                    A[v] = run_prod<false>(a, A[v]);
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                hl[j][v] = h[v];
-                Ap[j][v] = PACKED && cut ? -1.f : A[v];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = Ap[TS - 1][v];
-        float cin[V];
-        scan_exchange<V, PACKED>(sm, par, K, rank, A, h, carry, cin, [&] { load(t0 + step); });
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = run_map<PACKED>(Ap[j][v], hl[j][v], cin[v]);
-            if (live && t0 + j < p.T) st_vec<X, V>(y + (t0 + j) * p.y_st, o);
-            if (PACKED && (ends >> j & 1)) {
-                const int n = __shfl_sync(~0u, owner, j);
-                if (p.fin && live)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) p.fin[n * p.fin_sn + c + v] = o[v];
-            }
-        }
-    }
-    if (!PACKED && p.fin && live && rank == 0 && w == 0)
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.fin[b * p.fin_sn + c + v] = carry[v];
-}
-
-template <typename X, typename G, int V, int TS, bool PACKED>
-__global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd_tiled(ScanParams p, int K) {
-    __shared__ ScanSmem<V> sm;
-    const unsigned rank = K > 1 ? cluster_rank() : 0;
-    const int item = blockIdx.x / K, ct = (p.D + 32 * V - 1) / (32 * V);
-    const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = (item % ct) * 32 * V + lane * V;
-    const bool live = c < p.D;
-    const X* dh = static_cast<const X*>(p.x) + b * p.x_sb + c;
-    const X* hp = static_cast<const X*>(p.h) + b * p.h_sb + c;
-    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + c;
-    X* dx = static_cast<X*>(p.y) + b * p.y_sb + c;
-    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c;
-    if (PACKED) {
-        scan_check_cu(p);
-        scan_empty<V>(p, p.sT, p.sT_sn, c, K, rank);
-    }
-    float carry[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = !PACKED && live && p.sT ? p.sT[b * p.sT_sn + c + v] : 0.f;
-
-    typename RawVec<X, V>::T rd[TS], rh[TS];
-    typename RawVec<G, V>::T rg[TS];
-    const int step = K * kScanWarps * TS;
-    // token of this warp's place j in the tile: t0 - j
-    int64_t t0 = p.T - 1 - ((int64_t)rank * kScanWarps + w) * TS;
-    auto load = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            const bool in = live && t - j >= 0, prev = live && t - j >= 1;
-            rd[j] = in ? ld_raw<X, V>(dh + (t - j) * p.x_st) : typename RawVec<X, V>::T{};
-            rg[j] = in ? ld_raw<G, V>(g + (t - j) * p.g_st) : typename RawVec<G, V>::T{};
-            rh[j] = prev ? ld_raw<X, V>(hp + (t - j - 1) * p.h_st) : typename RawVec<X, V>::T{};
-        }
-    };
-    load(t0);
-    if (K > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    int par = 0;
-    for (int64_t tile = 0; tile < p.T; tile += step, t0 -= step, par ^= 1) {
-        unsigned starts = 0, ends = 0;
-        int owner = 0;
-        if (PACKED) {
-            const bool in = lane < TS && t0 - lane >= 0;
-            const int t = in ? (int)(t0 - lane) : 0;
-            owner = scan_owner(p.cu, p.N, t);
-            starts = __ballot_sync(~0u, in && p.cu[owner] == t);
-            ends = __ballot_sync(~0u, in && p.cu[owner + 1] == t + 1);
-        }
-        float dl[TS][V], Ae[TS][V], m[TS][V], A[V], e[V];
-        bool cut = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = 1.f, e[v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            float dv[V], gv[V], hv[V];
-            unpack(rd[j], dv);
-            unpack(rg[j], gv);
-            unpack(rh[j], hv);
-            if (PACKED && (ends >> j & 1)) {
-                cut = true;
-                const int n = __shfl_sync(~0u, owner, j);
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[v] = live && p.sT ? p.sT[n * p.sT_sn + c + v] : 0.f;
-            }
-            if (PACKED ? (starts >> j & 1) : t0 - j == 0) {
-                const int n = PACKED ? __shfl_sync(~0u, owner, j) : b;
-#pragma unroll
-                for (int v = 0; v < V; ++v) hv[v] = live && p.s0 ? p.s0[n * p.s0_sn + c + v] : 0.f;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float a = expf(gv[v]);
-                const float d = dv[v] + e[v];
-                dl[j][v] = d;
-                Ae[j][v] = PACKED && cut ? -1.f : A[v];
-                m[j][v] = a * hv[v];
-                e[v] = a * d;
-                A[v] = run_prod<false>(a, A[v]);
-            }
-        }
-        if (PACKED && cut)
-#pragma unroll
-            for (int v = 0; v < V; ++v) A[v] = -1.f;
-        float cin[V];
-        scan_exchange<V, PACKED>(sm, par, K, rank, A, e, carry, cin, [&] { load(t0 - step); });
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            float d[V], q[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                d[v] = run_map<PACKED>(Ae[j][v], dl[j][v], cin[v]);
-                q[v] = d[v] * m[j][v];
-            }
-            if (live && t0 - j >= 0) {
-                st_vec<X, V>(dx + (t0 - j) * p.y_st, d);
-                st_vec<G, V>(dg + (t0 - j) * p.dg_st, q);
-            }
-            if (PACKED && (starts >> j & 1)) {
-                const int n = __shfl_sync(~0u, owner, j);
-                if (p.fin && live)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        p.fin[n * p.fin_sn + c + v] = expf(ld_elem(g + (t0 - j) * p.g_st + v)) * d[v];
-            }
-        }
-    }
-    if (!PACKED && p.fin && live && rank == 0 && w == 0)
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.fin[b * p.fin_sn + c + v] = carry[v];
-}
-
-// ---- pairs of channels: tokens staged in shared memory ------------------------------------
-//
-// The same split with two channels per lane and the tokens of three tiles on their way
-// through shared memory (cp.async; a warp reads only what it copied itself).  Eight warps
-// form the (A, H) of tile i + 1 before they finish tile i; a ninth joins the warps' runs,
-// sends the CTA's to the cluster's other CTAs (st.async on their mbarriers), waits for theirs
-// and hands every warp the h before its run, all of it behind the finishing of the tile
-// before.  A tile is finished by running its recurrence again from the h that comes in (the
-// decays of an fp32 gate are left in its place in shared memory by the first pass; of a bf16
-// gate the power is taken twice).
 constexpr int kScanStages = 3;
-constexpr int kScanPipedThreads = kScanThreads + 32;
+constexpr int kScanPipedThreads = (kScanWarps + 1) * 32;
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
@@ -464,8 +179,10 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 
 // Copies the tokens of one warp's run into shared memory, tile after tile: rows j = 0 .. TS - 1
 // (token t + DIR * j; zeros outside 0 .. T - 1 and past channel D) of 64 channels from c0, 64
-// elements a row; 16 bytes a lane where addresses allow, else a lane's own pair.
-template <typename E, int TS, int DIR>
+// elements a row.  16 bytes a lane where addresses allow (wide); else, with EVEN, a lane's own
+// pair, without it the elements lane and lane + 32 (of bf16 through registers: the smallest
+// asynchronous copy has 4 bytes).
+template <typename E, int TS, int DIR, bool EVEN>
 struct ScanSrc {
     static constexpr int kPer = 64 * sizeof(E) / 16;        // lanes of a row at 16 bytes each
     const E* base;                                          // a readable address
@@ -474,10 +191,12 @@ struct ScanSrc {
     int row, left;                                          // its first row; bytes of the piece that exist
     bool wide;
     __device__ __forceinline__ ScanSrc(const E* p, int64_t st, int t, int step, int c0, int D, bool wide_) : wide(wide_) {
-        const int lane = threadIdx.x & 31, bytes = wide ? 16 : 2 * (int)sizeof(E);
+        const int lane = threadIdx.x & 31;
+        constexpr int es = sizeof(E);
         row = wide ? lane / kPer : 0;
-        const int c = c0 + (wide ? lane % kPer * (16 / (int)sizeof(E)) : lane * 2);
-        left = max(0, min(bytes, (D - c) * (int)sizeof(E)));
+        const int c = c0 + (wide ? lane % kPer * (16 / es) : EVEN ? lane * 2 : lane);
+        const int bytes = (D - c) * es;
+        left = max(0, wide ? min(16, bytes) : EVEN ? min(2 * es, bytes) : bytes);
         base = p;
         cur = p + c + (t + DIR * row) * st;
         inc = DIR * st * (wide ? 32 / kPer : 1);
@@ -485,6 +204,7 @@ struct ScanSrc {
     }
     // t: the tile's first token; inside: every row and channel of it exists
     __device__ __forceinline__ void copy(E* dst, int t, int T, bool inside) {
+        constexpr int es = sizeof(E);
         const int lane = threadIdx.x & 31;
         const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
         const E* src = cur;
@@ -499,16 +219,48 @@ struct ScanSrc {
                     cp_async<16>(d + i * 512 + lane * 16, in ? src : base, in ? left : 0);
                 }
             }
-        } else {
+        } else if constexpr (EVEN) {
 #pragma unroll
             for (int j = 0; j < TS; ++j, src += inc) {
                 const bool in = (unsigned)(t + DIR * j) < (unsigned)T && left > 0;
-                cp_async<2 * (int)sizeof(E)>(d + (j * 64 + lane * 2) * (int)sizeof(E), in ? src : base, in ? left : 0);
+                cp_async<2 * es>(d + (j * 64 + lane * 2) * es, in ? src : base, in ? left : 0);
             }
+        } else if constexpr (es == 4) {
+#pragma unroll
+            for (int j = 0; j < TS; ++j, src += inc) {
+                const bool in = (unsigned)(t + DIR * j) < (unsigned)T;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool is = in && left > h * 32 * es;
+                    cp_async<4>(d + (j * 64 + h * 32 + lane) * es, is ? src + h * 32 : base, is ? 4 : 0);
+                }
+            }
+        } else {
+            E f[TS][2];
+#pragma unroll
+            for (int j = 0; j < TS; ++j, src += inc)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    f[j][h] = (unsigned)(t + DIR * j) < (unsigned)T && left > h * 32 * es ? src[h * 32] : E(0.f);
+#pragma unroll
+            for (int j = 0; j < TS; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) dst[j * 64 + h * 32 + lane] = f[j][h];
         }
         cur += tile;
     }
 };
+
+// Two channels of a lane to global memory, as a pair or (EVEN false) as far as there are two.
+template <typename E, bool EVEN>
+__device__ __forceinline__ void scan_store(E* q, const float* f, bool second) {
+    if constexpr (EVEN) {
+        st_vec<E, 2>(q, f);
+    } else {
+        st_elem(q, f[0]);
+        if (second) st_elem(q + 1, f[1]);
+    }
+}
 
 // e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
 // relative in all, where a token's step needs no more: a decay's error enters h with weight a.
@@ -527,7 +279,6 @@ __device__ __forceinline__ float scan_pow2(float x) {
 struct ScanRuns {
     float4 warp[kScanWarps][32];          // (A0, A1, H0, H1) of each warp's run; then, in its
                                           // first half, what comes into the run
-    float4 cta[2][kScanMaxCluster][32];   // of each CTA's run
     uint64_t full[2];                     // the cluster's runs of a tile have arrived
 };
 
@@ -572,7 +323,7 @@ __device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity
 // The ninth warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
 // into the first tile, in the end what leaves the last one.
 template <bool PACKED, bool CL>
-__device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsigned rank, float* carry, int* err) {
+__device__ __forceinline__ void scan_join(ScanRuns& sm, float4* cta, int tiles, int K, unsigned rank, float* carry, int* err) {
     const int lane = threadIdx.x & 31;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
@@ -593,7 +344,7 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsign
                 all = run_join<PACKED>(sm.warp[w][lane], all);
             }
             if (lane == 0) sm100::mbar_expect_tx(&sm.full[par], K * 512);
-            const uint32_t dst = sm100::saddr(&sm.cta[par][rank][lane]), bar = sm100::saddr(&sm.full[par]);
+            const uint32_t dst = sm100::saddr(cta + (par * K + rank) * 32 + lane), bar = sm100::saddr(&sm.full[par]);
             for (int r = 0; r < K; ++r) {
                 uint32_t d, m;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dst), "r"(r));
@@ -608,7 +359,7 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, int tiles, int K, unsign
             float c0 = 0.f, c1 = 0.f;
             for (int r = 0; r < K; ++r) {
                 if (r == (int)rank) c0 = carry[0], c1 = carry[1];
-                run_through<PACKED>(sm.cta[par][r][lane], carry[0], carry[1]);
+                run_through<PACKED>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
             }
 #pragma unroll
             for (int w = 0; w < kScanWarps; ++w) {
@@ -681,22 +432,23 @@ struct ScanStage {
     X h[BWD ? 2 : 1][BWD ? kScanWarps : 1][BWD ? TS : 1][64];
 };
 
-template <typename X, typename G, int TS, bool PACKED, bool CL>
+template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN>
 __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    ScanStage<X, G, TS, false>& st = *reinterpret_cast<ScanStage<X, G, TS, false>*>(dyn);
+    using Stage = ScanStage<X, G, TS, false>;       // then [2][K][32] float4: the CTAs' runs
+    Stage& st = *reinterpret_cast<Stage*>(dyn);
     __shared__ ScanRuns sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
-    const bool live = c < p.D, whole = c0 + 64 <= p.D;
+    const bool live = c < p.D, live1 = EVEN || c + 1 < p.D, whole = c0 + 64 <= p.D;
     const int step = K * kScanWarps * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
     int t0 = ((int)rank * kScanWarps + w) * TS;              // this warp's first token of tile i
-    ScanSrc<X, TS, 1> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
-    ScanSrc<G, TS, 1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
+    ScanSrc<X, TS, 1, EVEN> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
+    ScanSrc<G, TS, 1, EVEN> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
     X* y = static_cast<X*>(p.y) + b * p.y_sb + c + t0 * p.y_st;
     const int64_t y_tile = (int64_t)step * p.y_st;
     auto load = [&](int t, int s) {
@@ -710,19 +462,19 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         for (int s = 0; s < kScanStages; ++s) load(t0 + s * step, s);
     if (PACKED) {
         scan_check_cu(p);
-        if (w < kScanWarps) scan_empty<2>(p, p.s0, p.s0_sn, c, K, rank);
+        if (w < kScanWarps) scan_empty(p, p.s0, p.s0_sn, c, K, rank);
     }
     scan_enter<CL>(sm);
     if (w == kScanWarps) {
         float carry[2] = {0.f, 0.f};
         if (!PACKED && live && p.s0) {
             carry[0] = p.s0[b * p.s0_sn + c];
-            carry[1] = p.s0[b * p.s0_sn + c + 1];
+            if (live1) carry[1] = p.s0[b * p.s0_sn + c + 1];
         }
-        scan_join<PACKED, CL>(sm, tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
-            p.fin[b * p.fin_sn + c + 1] = carry[1];
+            if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
         scan_leave<CL>();
         return;
@@ -731,16 +483,24 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
     auto initial = [&](int t, float* s) {      // the start state of the sequence that t starts
         const int n = scan_owner(p.cu, p.N, t);
         s[0] = live && p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
-        s[1] = live && p.s0 ? p.s0[n * p.s0_sn + c + 1] : 0.f;
+        s[1] = live && live1 && p.s0 ? p.s0[n * p.s0_sn + c + 1] : 0.f;
     };
     // the run of this warp's tokens of one tile
     auto form = [&](int t, int s, unsigned starts) {
         float h[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+        // all loads ahead of the first store, which they could not pass
+        typename RawVec<X, 2>::T rx[TS];
+        typename RawVec<G, 2>::T rg[TS];
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            rx[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
+            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
+        }
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             float xv[2], a[2];
-            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
-            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+            unpack(rx[j], xv);
+            unpack(rg[j], a);
             scan_log2(a);
             add2(L, a, L);
             a[0] = scan_pow2(a[0]);
@@ -756,11 +516,18 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
     auto finish = [&](int t, int s, unsigned starts, unsigned ends) {
         const int left = min(TS, p.T - t);
         X* o = y;
+        typename RawVec<X, 2>::T rx[TS];
+        typename RawVec<G, 2>::T rg[TS];
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            rx[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
+            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
+        }
 #pragma unroll
         for (int j = 0; j < TS; ++j, o += p.y_st) {
             float xv[2], a[2];
-            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), xv);
-            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+            unpack(rx[j], xv);
+            unpack(rg[j], a);
             if constexpr (sizeof(G) == 2) {
                 scan_log2(a);
                 a[0] = scan_pow2(a[0]);
@@ -768,17 +535,17 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
             }
             if (PACKED && (starts >> j & 1)) initial(t + j, cin);
             fma2(a, cin, xv, cin);
-            if (live && j < left) st_vec<X, 2>(o, cin);
+            if (live && j < left) scan_store<X, EVEN>(o, cin, live1);
             if (PACKED && (ends >> j & 1) && live && p.fin) {
                 float* f = p.fin + scan_owner(p.cu, p.N, t + j) * p.fin_sn + c;
                 f[0] = cin[0];
-                f[1] = cin[1];
+                if (live1) f[1] = cin[1];
             }
         }
         // the places past the last token hold a = 1, x = 0: they leave h as it is
         if (!PACKED && left > 0 && left >= p.T - t && live && p.fin) {
             p.fin[b * p.fin_sn + c] = cin[0];
-            p.fin[b * p.fin_sn + c + 1] = cin[1];
+            if (live1) p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
     ScanSeq seq;
@@ -819,23 +586,24 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
     scan_leave<CL>();
 }
 
-template <typename X, typename G, int TS, bool PACKED, bool CL>
+template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN>
 __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    ScanStage<X, G, TS, true>& st = *reinterpret_cast<ScanStage<X, G, TS, true>*>(dyn);
+    using Stage = ScanStage<X, G, TS, true>;       // then [2][K][32] float4: the CTAs' runs
+    Stage& st = *reinterpret_cast<Stage*>(dyn);
     __shared__ ScanRuns sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
-    const bool live = c < p.D, whole = c0 + 64 <= p.D;
+    const bool live = c < p.D, live1 = EVEN || c + 1 < p.D, whole = c0 + 64 <= p.D;
     const int step = K * kScanWarps * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
     int t0 = p.T - 1 - ((int)rank * kScanWarps + w) * TS;    // token of place j of tile i: t0 - j
-    ScanSrc<X, TS, -1> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
-    ScanSrc<G, TS, -1> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
-    ScanSrc<X, TS, -1> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, t0 - 1, step, c0, p.D, wide & 4);
+    ScanSrc<X, TS, -1, EVEN> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
+    ScanSrc<G, TS, -1, EVEN> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
+    ScanSrc<X, TS, -1, EVEN> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, t0 - 1, step, c0, p.D, wide & 4);
     X* dx = static_cast<X*>(p.y) + b * p.y_sb + c + t0 * p.y_st;
     G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c + t0 * p.dg_st;
     const int64_t dx_tile = (int64_t)step * p.y_st, dg_tile = (int64_t)step * p.dg_st;
@@ -854,19 +622,19 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         }
     if (PACKED) {
         scan_check_cu(p);
-        if (w < kScanWarps) scan_empty<2>(p, p.sT, p.sT_sn, c, K, rank);
+        if (w < kScanWarps) scan_empty(p, p.sT, p.sT_sn, c, K, rank);
     }
     scan_enter<CL>(sm);
     if (w == kScanWarps) {
         float carry[2] = {0.f, 0.f};
         if (!PACKED && live && p.sT) {
             carry[0] = p.sT[b * p.sT_sn + c];
-            carry[1] = p.sT[b * p.sT_sn + c + 1];
+            if (live1) carry[1] = p.sT[b * p.sT_sn + c + 1];
         }
-        scan_join<PACKED, CL>(sm, tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
-            p.fin[b * p.fin_sn + c + 1] = carry[1];
+            if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
         scan_leave<CL>();
         return;
@@ -874,15 +642,22 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
     float cin[2];
     auto state = [&](const float* src, int64_t sn, int n, float* s) {
         s[0] = live && src ? src[n * sn + c] : 0.f;
-        s[1] = live && src ? src[n * sn + c + 1] : 0.f;
+        s[1] = live && live1 && src ? src[n * sn + c + 1] : 0.f;
     };
     auto form = [&](int t, int s, unsigned ends) {
         float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+        typename RawVec<X, 2>::T rd[TS];
+        typename RawVec<G, 2>::T rg[TS];
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            rd[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
+            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
+        }
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             float dv[2], a[2];
-            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), dv);
-            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
+            unpack(rd[j], dv);
+            unpack(rg[j], a);
             scan_log2(a);
             add2(L, a, L);
             a[0] = scan_pow2(a[0]);
@@ -901,12 +676,20 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         const bool at0 = !PACKED && left > 0 && t < TS;
         X* ox = dx;
         G* og = dg;
+        typename RawVec<X, 2>::T rd[TS], rh[TS];
+        typename RawVec<G, 2>::T rg[TS];
+#pragma unroll
+        for (int j = 0; j < TS; ++j) {
+            rd[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
+            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
+            rh[j] = ld_raw<X, 2>(&st.h[hslot][w][j][lane * 2]);
+        }
 #pragma unroll
         for (int j = 0; j < TS; ++j, ox -= p.y_st, og -= p.dg_st) {
             float dv[2], a[2], hv[2];
-            unpack(ld_raw<X, 2>(&st.x[s][w][j][lane * 2]), dv);
-            unpack(ld_raw<G, 2>(&st.g[s][w][j][lane * 2]), a);
-            unpack(ld_raw<X, 2>(&st.h[hslot][w][j][lane * 2]), hv);
+            unpack(rd[j], dv);
+            unpack(rg[j], a);
+            unpack(rh[j], hv);
             if constexpr (sizeof(G) == 2) {
                 scan_log2(a);
                 a[0] = scan_pow2(a[0]);
@@ -921,18 +704,18 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
             mul2(a, d, cin);
             mul2(cin, hv, q);
             if (live && j < left) {
-                st_vec<X, 2>(ox, d);
-                st_vec<G, 2>(og, q);
+                scan_store<X, EVEN>(ox, d, live1);
+                scan_store<G, EVEN>(og, q, live1);
             }
             if (PACKED && (starts >> j & 1) && live && p.fin) {
                 p.fin[n * p.fin_sn + c] = cin[0];
-                p.fin[n * p.fin_sn + c + 1] = cin[1];
+                if (live1) p.fin[n * p.fin_sn + c + 1] = cin[1];
             }
         }
         // the places past token 0 hold a = 1, d = 0: they leave what comes in as it is
         if (at0 && live && p.fin) {
             p.fin[b * p.fin_sn + c] = cin[0];
-            p.fin[b * p.fin_sn + c + 1] = cin[1];
+            if (live1) p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
     ScanSeq seq;
