@@ -75,7 +75,7 @@ dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* c
         N = cu->shape[0] - 1;
         if (N >= (int64_t(1) << 24)) return DN_ERR_INVALID_ARG;
     }
-    if (N > 0 && (D + kScanThreads - 1) / kScanThreads > kMax31 / N) return DN_ERR_INVALID_ARG;
+    if (N > 0 && (D + kScanWalkers - 1) / kScanWalkers > kMax31 / N) return DN_ERR_INVALID_ARG;   // a grid's CTAs
     return DN_OK;
 }
 
@@ -112,7 +112,7 @@ bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
 // us; 256 of 2048 52, 59, 67, 88, 136 us; 128 of 256 6.3, 7.6, 10.5, 20, 49 us.
 int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
     int K = 1;
-    while (K < kScanMaxCluster && (items * K < sms * 7 / 8 || (K > 1 && items * K < sms * 4 / 3)) &&
+    while (K < kScanMaxCluster && (items * K < sms * 5 / 6 || (K > 1 && items * K < sms * 4 / 3)) &&
            (int64_t)K * tokens * (K < 4 ? 4 : 8) <= T)
         K *= 2;
     return K;
@@ -139,7 +139,11 @@ dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, c
     return cudaLaunchKernelEx(&cfg, kern, p, K, a...) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
 }
 
-constexpr int kScanSerialT = 32;   // up to so many tokens, one thread walks a channel
+// Up to so many tokens a thread walks its channels, and up to the larger number where that
+// fills the GPU (four CTAs of walkers on an SM).  2048 channels, bf16 with fp32 gates, walkers
+// against tiles: 32 tokens of 512 rows 47 and 151 us, 128 of 128 rows 47 and 65, 192 of 85 rows
+// 50 and 57, 512 of 32 rows 85 and 51; backward 32 of 512 80 and 225, 512 of 128 346 and 301.
+constexpr int kScanSerialT = 16, kScanSerialManyT = 192;
 
 // 16-byte copies: bit 0 for x, 1 for g, 2 for h.
 int scan_wide(const ScanParams& p, int32_t x, int32_t g) {
@@ -175,11 +179,19 @@ dn_status scan_run(const ScanParams& p, int32_t x, int32_t g, cudaStream_t strea
     by_types(x, g, [&](auto xt, auto gt) {
         using X = decltype(xt);
         using G = decltype(gt);
-        if (p.T <= kScanSerialT) {
-            const unsigned grid = (unsigned)((int64_t)p.N * ((p.D + kScanThreads - 1) / kScanThreads));
-            if constexpr (BWD) k_scan_bwd_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
-            else k_scan_serial<X, G><<<grid, kScanThreads, 0, stream>>>(p);
-        } else if (scan_pairs(p, x, g, BWD)) {
+        const bool even = scan_pairs(p, x, g, BWD);
+        const int V = even ? 2 : 1;
+        const int64_t walkers = (int64_t)p.N * ((p.D + kScanWalkers * V - 1) / (kScanWalkers * V));
+        if (p.T <= kScanSerialT || (p.T <= kScanSerialManyT && walkers >= 4 * sms)) {
+            const unsigned grid = (unsigned)walkers;
+            if constexpr (BWD) {
+                if (even) k_scan_bwd_serial<X, G, 2><<<grid, kScanWalkers, 0, stream>>>(p);
+                else k_scan_bwd_serial<X, G, 1><<<grid, kScanWalkers, 0, stream>>>(p);
+            } else {
+                if (even) k_scan_serial<X, G, 2><<<grid, kScanWalkers, 0, stream>>>(p);
+                else k_scan_serial<X, G, 1><<<grid, kScanWalkers, 0, stream>>>(p);
+            }
+        } else if (even) {
             st = p.cu ? scan_tiled<X, G, true, BWD, true>(p, sms, stream) : scan_tiled<X, G, false, BWD, true>(p, sms, stream);
         } else {
             st = p.cu ? scan_tiled<X, G, true, BWD, false>(p, sms, stream) : scan_tiled<X, G, false, BWD, false>(p, sms, stream);

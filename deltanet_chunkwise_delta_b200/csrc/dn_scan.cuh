@@ -44,49 +44,125 @@ __device__ __forceinline__ void scan_range(const ScanParams& p, int n, int& b, i
     t1 = p.cu ? min(max(p.cu[n + 1], t0), p.T) : p.T;
 }
 
-// One thread per (sequence, channel), token after token.
-template <typename X, typename G>
-__global__ void __launch_bounds__(kScanThreads) k_scan_serial(ScanParams p) {
+// e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
+// relative in all, where a token's step needs no more: a decay's error enters h with weight a.
+__device__ __forceinline__ void scan_log2(float* g) {
+    const float c[2] = {1.44269504f, 1.44269504f};
+    mul2(g, c, g);
+}
+__device__ __forceinline__ float scan_pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float scan_decay(float g) { return scan_pow2(g * 1.44269504f); }
+
+// ---- short sequences: a thread walks its channels, token after token ----------------------
+//
+// One thread per V channels of a sequence (2 where rows are made of pairs), the next kScanAhead
+// tokens of its loads in registers.  Nothing is exchanged; what bounds it is the loads in
+// flight, so it takes short rows, or so many that they fill the GPU.
+constexpr int kScanAhead = 8, kScanWalkers = 128;
+
+template <typename X, typename G, int V>
+__global__ void __launch_bounds__(kScanWalkers) k_scan_serial(ScanParams p) {
     scan_check_cu(p);
-    const int per = (p.D + kScanThreads - 1) / kScanThreads;
-    const int n = blockIdx.x / per, c = (blockIdx.x % per) * kScanThreads + threadIdx.x;
+    const int per = (p.D + kScanWalkers * V - 1) / (kScanWalkers * V);
+    const int n = blockIdx.x / per, c = ((blockIdx.x % per) * kScanWalkers + threadIdx.x) * V;
     if (c >= p.D) return;
     int b, t0, t1;
     scan_range(p, n, b, t0, t1);
-    const X* x = static_cast<const X*>(p.x) + b * p.x_sb + c;
-    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + c;
-    X* y = static_cast<X*>(p.y) + b * p.y_sb + c;
-    float h = p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
-    for (int t = t0; t < t1; ++t) {
-        h = fmaf(expf(ld_elem(g + t * p.g_st)), h, ld_elem(x + t * p.x_st));
-        st_elem(y + t * p.y_st, h);
+    const X* x = static_cast<const X*>(p.x) + b * p.x_sb + t0 * p.x_st + c;
+    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + t0 * p.g_st + c;
+    X* y = static_cast<X*>(p.y) + b * p.y_sb + t0 * p.y_st + c;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = p.s0 ? p.s0[n * p.s0_sn + c + v] : 0.f;
+    for (int t = t0; t < t1; t += kScanAhead) {
+        typename RawVec<X, V>::T rx[kScanAhead];
+        typename RawVec<G, V>::T rg[kScanAhead];
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j)
+            if (t + j < t1) {
+                rx[j] = ld_raw<X, V>(x + j * p.x_st);
+                rg[j] = ld_raw<G, V>(g + j * p.g_st);
+            }
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j)
+            if (t + j < t1) {
+                float xv[V], a[V];
+                unpack(rx[j], xv);
+                unpack(rg[j], a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = fmaf(scan_decay(a[v]), h[v], xv[v]);
+                st_vec<X, V>(y + j * p.y_st, h);
+            }
+        x += kScanAhead * p.x_st;
+        g += kScanAhead * p.g_st;
+        y += kScanAhead * p.y_st;
     }
-    if (p.fin) p.fin[n * p.fin_sn + c] = h;
+    if (p.fin)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.fin[n * p.fin_sn + c + v] = h[v];
 }
 
-template <typename X, typename G>
-__global__ void __launch_bounds__(kScanThreads) k_scan_bwd_serial(ScanParams p) {
+template <typename X, typename G, int V>
+__global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) {
     scan_check_cu(p);
-    const int per = (p.D + kScanThreads - 1) / kScanThreads;
-    const int n = blockIdx.x / per, c = (blockIdx.x % per) * kScanThreads + threadIdx.x;
+    const int per = (p.D + kScanWalkers * V - 1) / (kScanWalkers * V);
+    const int n = blockIdx.x / per, c = ((blockIdx.x % per) * kScanWalkers + threadIdx.x) * V;
     if (c >= p.D) return;
     int b, t0, t1;
     scan_range(p, n, b, t0, t1);
-    const X* dh = static_cast<const X*>(p.x) + b * p.x_sb + c;
-    const X* h = static_cast<const X*>(p.h) + b * p.h_sb + c;
-    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + c;
-    X* dx = static_cast<X*>(p.y) + b * p.y_sb + c;
-    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + c;
-    float carry = p.sT ? p.sT[n * p.sT_sn + c] : 0.f;
-    for (int t = t1 - 1; t >= t0; --t) {
-        const float a = expf(ld_elem(g + t * p.g_st));
-        const float before = t > t0 ? ld_elem(h + (t - 1) * p.h_st) : p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
-        const float d = ld_elem(dh + t * p.x_st) + carry;
-        carry = a * d;
-        st_elem(dx + t * p.y_st, d);
-        st_elem(dg + t * p.dg_st, carry * before);
+    const int64_t last = t1 - 1;
+    const X* dh = static_cast<const X*>(p.x) + b * p.x_sb + last * p.x_st + c;
+    const X* hp = static_cast<const X*>(p.h) + b * p.h_sb + (last - 1) * p.h_st + c;
+    const G* g = static_cast<const G*>(p.g) + b * p.g_sb + last * p.g_st + c;
+    X* dx = static_cast<X*>(p.y) + b * p.y_sb + last * p.y_st + c;
+    G* dg = static_cast<G*>(p.dg) + b * p.dg_sb + last * p.dg_st + c;
+    float e[V];                            // a_{t+1} delta_{t+1}
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = p.sT ? p.sT[n * p.sT_sn + c + v] : 0.f;
+    for (int t = t1 - 1; t >= t0; t -= kScanAhead) {
+        typename RawVec<X, V>::T rd[kScanAhead], rh[kScanAhead];
+        typename RawVec<G, V>::T rg[kScanAhead];
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j)
+            if (t - j >= t0) {
+                rd[j] = ld_raw<X, V>(dh - j * p.x_st);
+                rg[j] = ld_raw<G, V>(g - j * p.g_st);
+                if (t - j > t0) rh[j] = ld_raw<X, V>(hp - j * p.h_st);
+            }
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j)
+            if (t - j >= t0) {
+                float d[V], a[V], hv[V], q[V];
+                unpack(rd[j], d);
+                unpack(rg[j], a);
+                if (t - j > t0) {
+                    unpack(rh[j], hv);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) hv[v] = p.s0 ? p.s0[n * p.s0_sn + c + v] : 0.f;
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    d[v] += e[v];
+                    e[v] = scan_decay(a[v]) * d[v];
+                    q[v] = e[v] * hv[v];
+                }
+                st_vec<X, V>(dx - j * p.y_st, d);
+                st_vec<G, V>(dg - j * p.dg_st, q);
+            }
+        dh -= kScanAhead * p.x_st;
+        hp -= kScanAhead * p.h_st;
+        g -= kScanAhead * p.g_st;
+        dx -= kScanAhead * p.y_st;
+        dg -= kScanAhead * p.dg_st;
     }
-    if (p.fin) p.fin[n * p.fin_sn + c] = carry;
+    if (p.fin)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.fin[n * p.fin_sn + c + v] = e[v];
 }
 
 // ---- runs of tokens across warps and CTAs ------------------------------------------------
@@ -260,18 +336,6 @@ __device__ __forceinline__ void scan_store(E* q, const float* f, bool second) {
         st_elem(q, f[0]);
         if (second) st_elem(q + 1, f[1]);
     }
-}
-
-// e^g as a power of two: one product and the hardware's 2^x (2 ulp), (4 + 2.4 |g|) 2^-24
-// relative in all, where a token's step needs no more: a decay's error enters h with weight a.
-__device__ __forceinline__ void scan_log2(float* g) {
-    const float c[2] = {1.44269504f, 1.44269504f};
-    mul2(g, c, g);
-}
-__device__ __forceinline__ float scan_pow2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // A warp's run of tile i + 1 is written after it has read what comes into that of tile i: one
