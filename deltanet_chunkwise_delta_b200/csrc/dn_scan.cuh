@@ -805,10 +805,10 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
         const int s1 = s + 1 == kScanStages ? 0 : s + 1;
-        if (i + 1 < tiles) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            next(t0 - step, s1);
-        }
+        // x and g of tile i + 1 and h of tile i are there: the last tile waits for its h, too
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (i + 1 < tiles) next(t0 - step, s1);
+        else __syncwarp();
         if (PACKED && (starts | ends)) finish(t0, s, i & 1, starts, ends);
         else finish(t0, s, i & 1, 0u, 0u);
         __syncwarp();

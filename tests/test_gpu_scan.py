@@ -397,6 +397,24 @@ def test_capture_before_the_first_call_on_a_stream_is_refused_softly():
     assert torch.equal(out, dn.deltanet_scan_fwd(xs, gs, s0)[0])
 
 
+@pytest.mark.parametrize("B,T,D", [(1, 32768, 2048), (8, 4096, 2048), (1, 20000, 514)])
+def test_backward_under_load(B, T, D):
+    """Every d_g of a large call is a h_{t-1} times its d_x (which is rounded, and so is d_g:
+    2^-8 each): nothing is read before it has arrived, the first tokens of a row included,
+    which are worked on last."""
+    xs, gs, s0 = draw(1, 64, D, BF, F)
+    h = torch.randn((B, T, D), device=DEV).to(BF)
+    dh = torch.randn((B, T, D), device=DEV).to(BF)
+    g = gs.repeat(B, T // 64 + 1, 1)[:, :T].contiguous()
+    s0 = torch.randn((B, D), device=DEV)
+    for _ in range(3):
+        dx, dg, _ = dn.deltanet_scan_bwd(g, h, dh, s0)
+        before = torch.cat([s0[:, None], h[:, :-1].float()], 1)
+        want = g.exp() * before * dx.float()
+        assert ((dg - want).abs() <= 2.0 ** -7 * want.abs() + 1e-30).all()
+        del before, want, dx, dg
+
+
 def test_same_call_same_bits():
     xs, gs, s0 = draw(2, 3000, 260, BF, F)
     a, b = dn.deltanet_scan_fwd(xs, gs, s0), dn.deltanet_scan_fwd(xs, gs, s0)
