@@ -739,7 +739,7 @@ void dn_wait_settings(unsigned long long* wait_ns, int* stall_chunk) {
 
 dn_status dn_device_check(int& dev, int& sms) { return device_check(dev, sms); }
 
-dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag) {
+dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create) {
     {
         std::lock_guard<std::mutex> lk(g_mu);
         auto it = g_ws.find(std::make_pair(dev, stream));
@@ -747,6 +747,10 @@ dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag) {
             *flag = it->second.flag;
             return DN_OK;
         }
+    }
+    if (!create) {
+        *flag = nullptr;
+        return DN_OK;
     }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return DN_ERR_CUDA;

@@ -150,10 +150,14 @@ bool norm_by_length(const NormParams& p, bool wide, F f) {
     return norm_try<32, false, false>(p.d, f) || norm_try<0, false, false>(p.d, f) || norm_try<1, false, false>(p.d, f);
 }
 
+// More than 48 KB of shared memory has to be asked for: the same limit in every call (calls on
+// several host threads share the kernel's attribute), above what any of them needs.
+constexpr int kNormSmem = 217 * 1024;
 template <typename Kern>
 bool norm_smem(Kern* kern, int bytes) {
-    return bytes <= 40960 ||
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    return bytes <= 32768 ||
+           (bytes <= kNormSmem &&
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem) == cudaSuccess);
 }
 
 // CTAs of a kernel that the GPU holds at once (they walk the rows, so more would only queue).

@@ -65,7 +65,7 @@ dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* c
     const int64_t B = x->shape[0], T = x->shape[1], D = x->shape[2];
     if (B < 0 || T < 0 || D < 1 || D > kMax31 || T > kMax31 || B > kMax31) return DN_ERR_INVALID_ARG;
     if (T > 0 && B > kMax31 / T) return DN_ERR_INVALID_ARG;
-    if (T > kMax31 - 4096) return DN_ERR_INVALID_ARG;   // the kernels' token counters run past T by a few tiles
+    if (T > kMax31 - 16384) return DN_ERR_INVALID_ARG;   // the kernels' token counters run past T by a few tiles
     const int64_t dims[3] = {B, T, D};
     if (!view_ok(x, 3, dims, kF32 | kBf16)) return DN_ERR_INVALID_ARG;
     if (!view_ok(g, 3, dims, x->dtype == DN_F32 ? kF32 : kF32 | kBf16)) return DN_ERR_INVALID_ARG;
@@ -88,12 +88,10 @@ dn_status scan_common(ScanParams& p, const dn_tensor* x, const dn_tensor* g, con
     p.x = x->data; p.x_sb = x->stride[0]; p.x_st = x->stride[1];
     p.g = g->data; p.g_sb = g->stride[0]; p.g_st = g->stride[1];
     p.B = (int)x->shape[0]; p.T = (int)x->shape[1]; p.D = (int)x->shape[2]; p.N = (int)N;
-    // packed input reports its boundaries through the error word; without it only a wait
-    // inside a cluster that gave up would, and a capture that finds none goes on without
-    st = dn_stream_flag(dev, stream, &p.err);
-    if (!cu) return DN_OK;
-    p.cu = static_cast<const int*>(cu->data);
-    return st;
+    // packed input reports its boundaries through the error word; dense input would report a
+    // wait inside a cluster that gave up (its outputs are NaN then), where there is a word
+    if (cu) p.cu = static_cast<const int*>(cu->data);
+    return dn_stream_flag(dev, stream, &p.err, cu != nullptr);
 }
 
 // Pairs of channels can move as one access: even D, strides and addresses.
@@ -119,7 +117,7 @@ int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
 }
 
 template <typename Kern, typename... A>
-dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, cudaStream_t stream,
+dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, int most, cudaStream_t stream,
                       const ScanParams& p, A... a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * K));
@@ -132,7 +130,8 @@ dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, c
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = K > 1 ? 1 : 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // the same limit in every call: calls on several host threads share the kernel's attribute
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
         return DN_ERR_CUDA;
     if (K > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DN_ERR_CUDA;
@@ -166,7 +165,7 @@ dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     const int smem = stage + (K > 1 ? K * 1024 : 0);
     const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
     if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-    auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stream, p, wide); };
+    auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stage + kScanMaxCluster * 1024, stream, p, wide); };
     if constexpr (BWD) return K > 1 ? go(k_scan_bwd_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_bwd_piped<X, G, TS, PACKED, false, EVEN>);
     else return K > 1 ? go(k_scan_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_piped<X, G, TS, PACKED, false, EVEN>);
 }

@@ -328,8 +328,10 @@ __global__ void __launch_bounds__(kNormCta<TPR>, TPR == 0 ? 2 : 1) k_norm_fwd_ro
         param_part<TPR, VEC, SPLIT>(p.sc, l, d, 1.f, sc);
         param_part<TPR, VEC, SPLIT>(p.nw, l, d, 1.f, nw);
     }
-    if (VEC)                                           // what is never fetched reads as zeros
+    if (VEC) {                                         // what is never fetched reads as zeros
         for (int i = 0; i < 2 * Plan::all; ++i) ring_mem[i * TH + threadIdx.x] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     const int tpr = norm_tpr<TPR>(), nY = line_pieces<Y>(d), lines = 2 * nY + (RES ? line_pieces<R>(d) : 0);
     auto place = [&](int s, int k) {                   // lines: y, gate, residual one after another
         return VEC ? ring_mem + ((s * Plan::all + k) * TH + threadIdx.x)
@@ -448,8 +450,10 @@ __global__ void __launch_bounds__(kNormCta<TPR>, TPR <= 1 || TPR == 512 ? 1 : TP
                    : ring + ((s * ROWS + in_row) * lines +
                              (k < Plan::r ? k / Plan::nY * nY : 3 * nY + (k == Plan::r ? 0 : nR)));
     };
-    if (VEC)                                           // what is never fetched reads as zeros
+    if (VEC) {                                         // what is never fetched reads as zeros
         for (int i = 0; i < 2 * Plan::all; ++i) ring[i * TH + threadIdx.x] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     auto fetch = [&](const RowAt<SAME>& at, bool on, int s) {
         if constexpr (VEC) {
             if (on) {

@@ -420,6 +420,8 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, float4* cta, int tiles, 
                     : "memory");
             }
             ok = ok && cluster_mbar_wait(&sm.full[par], i >> 1 & 1);
+            // without the others' runs nothing after them is known: NaN, not numbers of some kind
+            if (!ok) carry[0] = carry[1] = __uint_as_float(0x7fffffffu);
             float c0 = 0.f, c1 = 0.f;
             for (int r = 0; r < K; ++r) {
                 if (r == (int)rank) c0 = carry[0], c1 = carry[1];
