@@ -197,6 +197,21 @@ def test_nan_and_inf_stay_in_their_row():
         assert torch.isnan(b[0][2]).all() and not torch.isfinite(gb.d_weight).all()
 
 
+def test_infinite_weight_with_fewer_rows_than_a_cta_takes():
+    """y1 is infinite in one column, and so is that column of d_scale; the places of rows that
+    a CTA has room for and the call does not have add nothing (0 times inf would be NaN)."""
+    for d in (64, 65, 128, 256):
+        c = draw((3, d), "wrs")
+        c["y"], c["dr"] = c["y"].abs() + 0.5, c["dr"].abs() + 0.5
+        base = backward(c)
+        c["w"][5] = float("inf")
+        gr = backward(c)
+        assert gr.d_scale[5] == float("inf")
+        rest = [i for i in range(d) if i != 5]
+        assert torch.equal(gr.d_scale[rest], base.d_scale[rest])
+        assert torch.equal(gr.d_residual, base.d_residual)
+
+
 def test_extreme_gates_and_zero_rows():
     """Gates far out (the sigmoid is 0 or 1 there), rows of zeros (rstd is eps^-1/2)."""
     c = draw((6, 64), "wz")
