@@ -219,6 +219,7 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
     const int64_t N = q->shape[0], T = q->shape[1], H = q->shape[2], dk = q->shape[3], dv = v->shape[3];
     if (N < 0 || T < 0 || H < 0 || dk < 1 || dv < 1) return DN_ERR_INVALID_ARG;
     if (N > kMax31 || T > kMax31 / n_h || H >= 65536) return DN_ERR_INVALID_ARG;
+    if (T > 0 && N > kMax31 / (T * n_h)) return DN_ERR_INVALID_ARG;
     const int64_t Tw = T * n_h, M = state->shape[0];
     const int64_t kd[4] = {N, Tw, H, dk}, vd[4] = {N, Tw, H, dv}, od[4] = {N, T, H, dv}, bd[3] = {N, Tw, H};
     const int64_t sd[4] = {M, H, dk, dv}, gd[4] = {N, T, H, dk};

@@ -321,7 +321,8 @@ dn_status deltanet_fwd_noalloc(const dn_tensor* q, const dn_tensor* k, const dn_
  *                 deltanet_get_error.
  *   out           [N, T, H, d_v], dtype of q; fully overwritten
  *
- * Supported head dims: d_k, d_v in {64, 128}, bf16 and fp32.  N, T or H may be 0.
+ * Supported head dims: d_k, d_v in {64, 128}, bf16 and fp32.  N, T or H may be 0; N T n_h
+ * stays below 2^31 and H below 65536.
  * The state stays in registers for all T tokens and is read and written once.
  * Layout rules as deltanet_fwd; state rows may not overlap each other.  state and
  * out may not overlap each other or any input (DN_ERR_ALIAS).  With
@@ -361,7 +362,8 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
  * cu_seqlens the call uses its stream's error word (see deltanet_step).  With
  * cu_seqlens contents that deltanet_get_error reports as DN_ERR_SEQLENS the outputs
  * are unspecified.  The result does not depend on timing: the same call gives the
- * same bits.
+ * same bits.  (Long rows are split across a thread-block cluster; a wait in it that
+ * gave up after 2 s would leave NaN behind it.)
  */
 dn_status deltanet_scan_fwd(const dn_tensor* x, const dn_tensor* g,
                             const dn_tensor* initial_state, const dn_tensor* cu_seqlens,
@@ -376,7 +378,7 @@ dn_status deltanet_scan_fwd(const dn_tensor* x, const dn_tensor* g,
  *
  *   g, initial_state, cu_seqlens   as given to the forward call
  *   out             [B, T, D] the forward call's output: h_{t-1} in d_g is read from
- *                   it as stored (bf16: rounded, 2^-9 relative in d_g)
+ *                   it as stored (bf16: rounded, 2^-8 relative in d_g)
  *   d_out           [B, T, D], dtype of out
  *   d_final_state   [N, D] fp32, or NULL for zeros
  *   d_x, d_g        [B, T, D], dtypes of out and g; fully overwritten

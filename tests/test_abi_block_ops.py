@@ -74,6 +74,7 @@ def test_step_refusals(lib):
     assert s(lib, out=desc([3, 2, 2, 64], at=1)) == ALIAS
     assert s(lib, slot_idx=desc([3], L.DN_I32, 6, off=64)) == ALIAS
     assert Step(dk=96)(lib) == UNS and Step(dv=256)(lib) == UNS
+    assert Step(N=2**16, T=2**15, H=1, nh=1, M=2**16)(lib) == ARG            # N T n_h reaches 2^31
     assert Step(N=2**20, T=0, H=2**12, M=2**20)(lib, slot_idx=None) == ARG   # more CTAs than a grid has
 
 
