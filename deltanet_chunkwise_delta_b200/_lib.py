@@ -425,6 +425,9 @@ def _descriptors(*tensors):
 
 
 _HERE = contextlib.nullcontext()
+# The current stream's handle without a Stream object around it, where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda idx: torch.cuda.current_stream(idx).cuda_stream)
 
 
 def _place(name, stream, lead, *others):
@@ -441,7 +444,7 @@ def _place(name, stream, lead, *others):
             raise ValueError(f"{name}: tensors on {lead.device}, stream on {stream.device}")
         return stream.cuda_stream, torch.cuda.stream(stream)
     here = _HERE if torch.cuda.current_device() == idx else torch.cuda.device(idx)
-    return torch.cuda.current_stream(idx).cuda_stream, here
+    return _raw_stream(idx), here
 
 
 def _like(t: torch.Tensor) -> torch.Tensor:
@@ -603,7 +606,8 @@ def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
                           next_weight, d_residual_out, d_y, d_gate, d_residual)
     with here:
         dev, lib = y.device, load()
-        like = lambda t, given: given if given is not None or t is None else             torch.empty(t.shape, dtype=t.dtype, device=dev)
+        like = lambda t, given: given if given is not None or t is None else \
+            torch.empty(t.shape, dtype=t.dtype, device=dev)
         d_y, d_gate, d_residual = like(y, d_y), like(gate, d_gate), like(residual, d_residual)
         params = [t is not None for t in (weight, scale, next_weight)]
         d, work, sums = y.shape[-1], None, [None] * 3
@@ -612,8 +616,7 @@ def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
             n = int(lib.deltanet_norm_workspace(y.numel() // d if d else 0, d))
             work = torch.empty(n, dtype=torch.float32, device=dev) if n else None
         a = _descriptors(y, weight, gate, residual, scale, next_weight, d_out,
-                               d_residual_out, d_y, sums[0], d_gate, d_residual, sums[1], sums[2],
-                               work)
+                         d_residual_out, d_y, sums[0], d_gate, d_residual, sums[1], sums[2], work)
         _check(lib.deltanet_norm_bwd(*a[:3], act, *a[3:6], float(eps), *a[6:], handle))
     return NormGrads(d_y, sums[0], d_gate, d_residual, sums[1], sums[2])
 

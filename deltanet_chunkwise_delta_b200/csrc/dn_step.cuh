@@ -3,7 +3,10 @@
 //
 // Column b of k S, u, S and o depends only on column b of S, so a CTA takes 32 columns
 // of one (request, head) and keeps its DK x 32 block of S in registers for all tokens:
-// one read and one write of the state, which is nearly all the bytes there are.
+// one read and one write of the state, which is nearly all the bytes there are.  B200: 256
+// requests of 16 heads of 128 x 128 take 87 us, 95 % of the measured copy rate; one request
+// alone 2.5 us, the latency of its chain of loads.  Four tokens of 33 requests (8 heads, 64 x
+// 128, fp32) take 8.7 us, 33 %: the tokens' sums and barriers one after another.
 #pragma once
 
 #include "dn_common.cuh"
