@@ -104,14 +104,14 @@ bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
 }
 
 // CTAs per cluster: enough for most SMs, and on to one and a third of them where a row is
-// split anyway (a cluster's CTAs often sit two to an SM), each with two tiles or more, four in
-// large clusters, whose start and exchange cost more.  Measured with 1, 2, 4, 8, 16: 32
-// channel tiles of 16384 tokens 207, 122, 67, 64, 89 us; 16 of 32768 414, 238, 126, 112, 105
-// us; 256 of 2048 52, 59, 67, 88, 136 us; 128 of 256 6.3, 7.6, 10.5, 20, 49 us.
+// split anyway (a cluster's CTAs often sit two to an SM), each with one and a half tiles or
+// more.  Measured with 1, 2, 4, 8 (forward, bf16, fp32 gates): 16 channel tiles of 32768 tokens
+// 415, 201, 105, 87 us; 32 of 16384 208, 104, 57, 52; 64 of 512 9.3, 8.8, 7.9, 11.5; 256 of
+// 2048 51, 56, 67, 94; 128 of 1024 17, 18, 24, 29 us.
 int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
     int K = 1;
     while (K < kScanMaxCluster && (items * K < sms * 5 / 6 || (K > 1 && items * K < sms * 4 / 3)) &&
-           (int64_t)K * tokens * (K < 4 ? 4 : 8) <= T)
+           (int64_t)K * tokens * 3 <= T)
         K *= 2;
     return K;
 }
@@ -132,8 +132,6 @@ dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, i
     cfg.numAttrs = K > 1 ? 1 : 0;
     // the same limit in every call: calls on several host threads share the kernel's attribute
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-        return DN_ERR_CUDA;
-    if (K > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DN_ERR_CUDA;
     return cudaLaunchKernelEx(&cfg, kern, p, K, a...) == cudaSuccess ? DN_OK : DN_ERR_CUDA;
 }
@@ -157,17 +155,30 @@ int scan_wide(const ScanParams& p, int32_t x, int32_t g) {
 template <typename X, typename G, bool PACKED, bool BWD, bool EVEN>
 dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 63) / 64);
-    // tokens of a warp's run: as many as leave room for two CTAs on an SM
-    constexpr int TS = sizeof(X) == 4 ? 4 : sizeof(G) == 2 && !BWD ? 16 : 8;
-    constexpr int stage = (int)sizeof(ScanStage<X, G, TS, BWD>);
-    static_assert(2 * (stage + 8192 + sizeof(ScanRuns) + 1024) <= 228 * 1024, "two CTAs on an SM, clusters of 8");
-    const int K = scan_cluster(items, p.T, kScanWarps * TS, sms);
-    const int smem = stage + (K > 1 ? K * 1024 : 0);
+    // Held runs where the instructions bound the tiles, and tokens per run as many as registers
+    // or two CTAs' shared memory allow.  Held and read twice: rows of one CTA, 8 x 2048 x 2048,
+    // bf16 gates 38 and 43 us, fp32 gates 53 and 50, all fp32 74 and 70; clusters of 8, 65536 x
+    // 2048 all fp32 270 and 333, 222464 x 2048 all bf16 484 and 586 us; backward 65536 x 2048
+    // 339 and 335, 8 x 2048 x 2048 93 and 90 us.
+    constexpr bool H1 = !BWD && sizeof(G) == 2, HK = !BWD;
+    constexpr int T1 = sizeof(X) == 4 ? 4 : 8, TK = T1 + (HK && EVEN ? 4 : 0);
+    constexpr int W1 = kScanWarps<H1>, WK = kScanWarps<HK>;
+    constexpr int stage = (int)sizeof(ScanStage<X, G, T1, BWD, W1>), part = (int)sizeof(ScanStage<X, G, TK, BWD, WK>);
+    static_assert(2 * (stage + sizeof(ScanRuns<W1>) + 1024) <= 228 * 1024 &&
+                  2 * (part + 8192 + sizeof(ScanRuns<WK>) + 1024) <= 228 * 1024, "two CTAs on an SM, clusters of 8");
+    const int K = scan_cluster(items, p.T, WK * TK, sms);
     const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
     if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
-    auto go = [&](auto* kern) { return scan_launch(kern, items, K, kScanPipedThreads, smem, stage + kScanMaxCluster * 1024, stream, p, wide); };
-    if constexpr (BWD) return K > 1 ? go(k_scan_bwd_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_bwd_piped<X, G, TS, PACKED, false, EVEN>);
-    else return K > 1 ? go(k_scan_piped<X, G, TS, PACKED, true, EVEN>) : go(k_scan_piped<X, G, TS, PACKED, false, EVEN>);
+    auto go = [&](auto* kern, int threads, int smem, int most) { return scan_launch(kern, items, K, threads, smem, most, stream, p, wide); };
+    if (K > 1) {
+        constexpr int th = kScanThreadsOf<HK>;
+        const int smem = part + K * 1024, most = part + kScanMaxCluster * 1024;
+        if constexpr (BWD) return go(k_scan_bwd_piped<X, G, TK, PACKED, true, EVEN, HK>, th, smem, most);
+        else return go(k_scan_piped<X, G, TK, PACKED, true, EVEN, HK>, th, smem, most);
+    }
+    constexpr int th = kScanThreadsOf<H1>;
+    if constexpr (BWD) return go(k_scan_bwd_piped<X, G, T1, PACKED, false, EVEN, H1>, th, stage, stage);
+    else return go(k_scan_piped<X, G, T1, PACKED, false, EVEN, H1>, th, stage, stage);
 }
 
 template <bool BWD>

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) 
 // ---- runs of tokens across warps and CTAs ------------------------------------------------
 //
 // A cluster of K CTAs takes 64 channels of one batch row (or of the packed tokens), two per
-// lane, and walks the tokens in tiles of K * 8 * TS, each warp TS tokens of a tile.  A run of
+// lane, and walks the tokens in tiles of K * W * TS, each of W warps TS tokens of a tile.  A run of
 // tokens maps the h before it to A h + H; a warp forms its run's (A, H), warps and CTAs
 // exchange theirs, and each then knows the h before its run and finishes its tokens.  Every
 // element is read once and written once.  Backward walks the tokens from the last one, with
@@ -179,19 +179,26 @@ __global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) 
 // A = -1 marks it (products of decays are >= 0).
 //
 // The tokens come through shared memory (cp.async; a warp reads only what it copied itself).
-// Eight warps form the (A, H) of tile i + 1 before they finish tile i; a ninth joins the
-// warps' runs, sends the CTA's to the cluster's other CTAs (st.async on their mbarriers),
-// waits for theirs and hands every warp the h before its run, all of it behind the finishing
-// of the tile before.  A tile is finished by running its recurrence again from the h that
-// comes in (the decays of an fp32 gate are left in its place in shared memory by the first
-// pass; of a bf16 gate the power is taken twice).
+// The warps form the (A, H) of tile i + 1 before they finish tile i; one more warp joins the
+// runs, sends the CTA's to the cluster's other CTAs (st.async on their mbarriers), waits for
+// theirs and hands every warp the h before its run, all of it behind the finishing of the tile
+// before.  A tile is finished by running its recurrence again from the h that comes in.  Its
+// tokens and decays stay in registers until then (HELD: seven warps and the joining one, 128
+// registers), or are read again (eight and one, 96 registers; the decays of an fp32 gate have
+// taken its place in shared memory, of a bf16 gate the power is taken twice): fewer
+// instructions and longer runs against one warp more.
 //
 // B200: forward of 8 x 2048 x 2048 (bf16, fp32 gates) 51 us, 80 % of the measured copy rate
-// (256 CTAs: 108 SMs have two of them, 40 have one); backward of 65536 x 2048 341 us,
-// 84 %; packed forward of 222459 x 2048 with bf16 gates 657 us, 63 %: without its loads and
-// stores it takes 469, the instructions and shared-memory accesses of the two passes bound it.
-constexpr int kScanWarps = 8;
-constexpr int kScanMaxCluster = 16;
+// (256 CTAs: 108 SMs have two of them, 40 have one); of 65536 x 2048 in fp32 270 us, 91 %;
+// backward of 65536 x 2048 (bf16, fp32 gates) 335 us, 85 %.  Packed forward of 222459 x 2048 in
+// bf16 565 us, 74 %; without the 32 sequences' boundaries 484: a tile with one goes the long
+// way in one warp, and the cluster waits for it.
+
+template <bool HELD>
+constexpr int kScanWarps = HELD ? 7 : 8;
+template <bool HELD>
+constexpr int kScanThreadsOf = (kScanWarps<HELD> + 1) * 32;
+constexpr int kScanMaxCluster = 8;
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -217,23 +224,13 @@ __device__ __forceinline__ float run_prod(float A, float B) {
     return PACKED && (A < 0.f || B < 0.f) ? -1.f : x;
 }
 
-// The last n with cu[n] <= t, in 0 .. N - 1 whatever cu holds.
-__device__ __forceinline__ int scan_owner(const int* cu, int N, int t) {
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Packed input: state rows of sequences without tokens (forward: final = initial state;
 // backward: d_initial = d_final).
+template <int W>
 __device__ __forceinline__ void scan_empty(const ScanParams& p, const float* src, int64_t src_sn, int c, int K,
                                            unsigned rank) {
     if (!p.fin) return;
-    for (int n = rank * kScanWarps + (threadIdx.x >> 5); n < p.N; n += K * kScanWarps)
+    for (int n = rank * W + (threadIdx.x >> 5); n < p.N; n += K * W)
         if (p.cu[n] >= p.cu[n + 1])
 #pragma unroll
             for (int v = 0; v < 2; ++v)
@@ -241,7 +238,6 @@ __device__ __forceinline__ void scan_empty(const ScanParams& p, const float* src
 }
 
 constexpr int kScanStages = 3;
-constexpr int kScanPipedThreads = (kScanWarps + 1) * 32;
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
@@ -343,8 +339,9 @@ __device__ __forceinline__ void scan_store(E* q, const float* f, bool second) {
 
 // A warp's run of tile i + 1 is written after it has read what comes into that of tile i: one
 // place.  The other CTAs may be a tile ahead: theirs go by tile parity.
+template <int W>
 struct ScanRuns {
-    float4 warp[kScanWarps][32];          // (A0, A1, H0, H1) of each warp's run; then, in its
+    float4 warp[W][32];                   // (A0, A1, H0, H1) of each warp's run; then, in its
                                           // first half, what comes into the run
     uint64_t full[2];                     // the cluster's runs of a tile have arrived
 };
@@ -387,26 +384,26 @@ __device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity
     }
 }
 
-// The ninth warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
+// The last warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
 // into the first tile, in the end what leaves the last one.
-template <bool PACKED, bool CL>
-__device__ __forceinline__ void scan_join(ScanRuns& sm, float4* cta, int tiles, int K, unsigned rank, float* carry, int* err) {
+template <bool PACKED, bool CL, int W>
+__device__ __forceinline__ void scan_join(ScanRuns<W>& sm, float4* cta, int tiles, int K, unsigned rank, float* carry, int* err) {
     const int lane = threadIdx.x & 31;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
         const int par = i & 1;
-        bar_sync(kBarRuns, kScanPipedThreads);
+        bar_sync(kBarRuns, (W + 1) * 32);
         if constexpr (!CL) {
 #pragma unroll
-            for (int w = 0; w < kScanWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float4 run = sm.warp[w][lane];
                 *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(carry[0], carry[1]);
                 run_through<PACKED>(run, carry[0], carry[1]);
             }
         } else {
-            float4 pre[kScanWarps], all = make_float4(1.f, 1.f, 0.f, 0.f);
+            float4 pre[W], all = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kScanWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 pre[w] = all;
                 all = run_join<PACKED>(sm.warp[w][lane], all);
             }
@@ -431,21 +428,21 @@ __device__ __forceinline__ void scan_join(ScanRuns& sm, float4* cta, int tiles, 
                 run_through<PACKED>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
             }
 #pragma unroll
-            for (int w = 0; w < kScanWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 float x0 = c0, x1 = c1;
                 run_through<PACKED>(pre[w], x0, x1);
                 *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
             }
         }
-        bar_arrive(kBarCin, kScanPipedThreads);
+        bar_arrive(kBarCin, (W + 1) * 32);
     }
     if (!ok && lane == 0 && err) *err = kErrTimeout;
 }
 
 // Before and after the work of a CTA of a cluster: barriers of the exchange ready everywhere,
 // nobody's memory gone while another CTA may still write to it.
-template <bool CL>
-__device__ __forceinline__ void scan_enter(ScanRuns& sm) {
+template <bool CL, int W>
+__device__ __forceinline__ void scan_enter(ScanRuns<W>& sm) {
     if (CL && threadIdx.x == 0) {
         sm100::mbar_init(&sm.full[0], 1);
         sm100::mbar_init(&sm.full[1], 1);
@@ -466,56 +463,79 @@ __device__ __forceinline__ void scan_leave() {
     }
 }
 
-// Packed input: which of a warp's tokens start or end a sequence.  (lo, hi) is the last
-// sequence looked up; tokens well inside it need no search.
+// The last n with cu[n] <= t, looked for outwards from `near`; in 0 .. N - 1 whatever cu holds.
+__device__ __forceinline__ int scan_owner_near(const int* cu, int N, int t, int near) {
+    int lo = near, hi = near;
+    if (cu[near] <= t) {
+        for (int d = 1; (hi = min(near + d, N)) < N && cu[hi] <= t; d *= 2) lo = hi;
+    } else {
+        for (int d = 1; (lo = max(near - d, 0)) > 0 && cu[lo] > t; d *= 2) hi = lo;
+    }
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Packed input: which of a warp's tokens start or end a sequence.  Tiles come in the order of
+// the walk, and those short of the far end (`edge`) of the last sequence looked up, n, need no
+// search.
+template <int TS, int DIR>
 struct ScanSeq {
-    int lo = 0, hi = 0;
+    int edge = DIR > 0 ? 0 : 0x7fffffff, n = 0, own = 0;
     unsigned starts = 0, ends = 0;
-    template <int TS, int DIR>
-    __device__ __forceinline__ void find(const ScanParams& p, int t0) {
-        const int a = DIR > 0 ? t0 : t0 - (TS - 1), b = a + TS;    // tokens [a, b)
+    // the sequence of this lane's token (lanes past the last one: of the last) of the tile at t0
+    __device__ __forceinline__ int owner(const ScanParams& p, int t0) const {
+        const int lane = threadIdx.x & 31, t = t0 + DIR * (lane < TS ? lane : TS - 1);
+        return scan_owner_near(p.cu, p.N, t < 0 ? 0 : t < p.T ? t : p.T - 1, n);
+    }
+    // s: the states that sequences begin with, in the order of the walk (or null): the next
+    // one's is asked for here, long before it is needed
+    __device__ __forceinline__ void find(const ScanParams& p, int t0, const float* s, int64_t sn, int c) {
         starts = ends = 0;
-        if (a > lo && b < hi) return;
-        const int lane = threadIdx.x & 31;
-        const int tl = t0 + DIR * (lane < TS ? lane : TS - 1);
-        const int t = tl < 0 ? 0 : tl < p.T ? tl : p.T - 1;
-        const int n = scan_owner(p.cu, p.N, t);
-        const bool in = lane < TS && tl >= 0 && tl < p.T;
-        const int s = p.cu[n], e = p.cu[n + 1];
-        starts = __ballot_sync(~0u, in && s == t);
+        if (DIR > 0 ? t0 + TS < edge : t0 - (TS - 1) > edge) return;
+        const int lane = threadIdx.x & 31, t = t0 + DIR * lane;
+        own = owner(p, t0);
+        const bool in = lane < TS && t >= 0 && t < p.T;
+        const int first = p.cu[own], e = p.cu[own + 1];
+        starts = __ballot_sync(~0u, in && first == t);
         ends = __ballot_sync(~0u, in && e == t + 1);
-        lo = __shfl_sync(~0u, s, TS - 1);
-        hi = __shfl_sync(~0u, e, TS - 1);
+        edge = __shfl_sync(~0u, DIR > 0 ? e : first, TS - 1);
+        n = __shfl_sync(~0u, own, TS - 1);
+        const int next = n + DIR;
+        if (s && next >= 0 && next < p.N && c < p.D) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + next * sn + c));
     }
 };
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The tokens on their way, a warp's rows together.  h is read only when a tile is finished,
-// one tile later than x and g: two stages of it are enough.
-template <typename X, typename G, int TS, bool BWD>
+// The tokens on their way, a warp's rows together.
+template <typename X, typename G, int TS, bool BWD, int W>
 struct ScanStage {
-    G g[kScanStages][kScanWarps][TS][64];
-    X x[kScanStages][kScanWarps][TS][64];
-    X h[BWD ? 2 : 1][BWD ? kScanWarps : 1][BWD ? TS : 1][64];
+    G g[kScanStages][W][TS][64];
+    X x[kScanStages][W][TS][64];
+    X h[BWD ? kScanStages : 1][BWD ? W : 1][BWD ? TS : 1][64];
 };
 
-template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN>
-__global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams p, int K, int wide) {
+template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN, bool HELD>
+__global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    using Stage = ScanStage<X, G, TS, false>;       // then [2][K][32] float4: the CTAs' runs
+    constexpr int W = kScanWarps<HELD>;
+    using Stage = ScanStage<X, G, TS, false, W>;       // then [2][K][32] float4: the CTAs' runs
     Stage& st = *reinterpret_cast<Stage*>(dyn);
-    __shared__ ScanRuns sm;
+    __shared__ ScanRuns<W> sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
     const bool live = c < p.D, live1 = EVEN || c + 1 < p.D, whole = c0 + 64 <= p.D;
-    const int step = K * kScanWarps * TS;
+    const int step = K * W * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
-    int t0 = ((int)rank * kScanWarps + w) * TS;              // this warp's first token of tile i
+    int t0 = ((int)rank * W + w) * TS;              // this warp's first token of tile i
     ScanSrc<X, TS, 1, EVEN> xs(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
     ScanSrc<G, TS, 1, EVEN> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
     X* y = static_cast<X*>(p.y) + b * p.y_sb + c + t0 * p.y_st;
@@ -526,21 +546,21 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         gs.copy(&st.g[s][w][0][0], t, p.T, inside);
         cp_async_commit();
     };
-    if (w < kScanWarps)
+    if (w < W)
 #pragma unroll
         for (int s = 0; s < kScanStages; ++s) load(t0 + s * step, s);
     if (PACKED) {
         scan_check_cu(p);
-        if (w < kScanWarps) scan_empty(p, p.s0, p.s0_sn, c, K, rank);
+        if (w < W) scan_empty<W>(p, p.s0, p.s0_sn, c, K, rank);
     }
-    scan_enter<CL>(sm);
-    if (w == kScanWarps) {
-        float carry[2] = {0.f, 0.f};
-        if (!PACKED && live && p.s0) {
-            carry[0] = p.s0[b * p.s0_sn + c];
-            if (live1) carry[1] = p.s0[b * p.s0_sn + c + 1];
-        }
-        scan_join<PACKED, CL>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
+    scan_enter<CL, W>(sm);
+    float cin[2], carry[2] = {0.f, 0.f};
+    if (!PACKED && live && p.s0) {
+        carry[0] = p.s0[b * p.s0_sn + c];
+        if (live1) carry[1] = p.s0[b * p.s0_sn + c + 1];
+    }
+    if (w == W) {
+        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
@@ -548,67 +568,75 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
         scan_leave<CL>();
         return;
     }
-    float cin[2];
-    auto initial = [&](int t, float* s) {      // the start state of the sequence that t starts
-        const int n = scan_owner(p.cu, p.N, t);
+    auto initial = [&](int n, float* s) {      // the start state of sequence n
         s[0] = live && p.s0 ? p.s0[n * p.s0_sn + c] : 0.f;
         s[1] = live && live1 && p.s0 ? p.s0[n * p.s0_sn + c + 1] : 0.f;
     };
     // the run of this warp's tokens of one tile
-    auto form = [&](int t, int s, unsigned starts) {
-        float h[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
-        // all loads ahead of the first store, which they could not pass
-        typename RawVec<X, 2>::T rx[TS];
-        typename RawVec<G, 2>::T rg[TS];
+    using GR = typename RawVec<G, 2>::T;
+    struct Held {                              // the tokens of a run
+        typename RawVec<X, 2>::T x[TS];
+        float a[TS][2];
+    };
+    // all of a run's loads ahead of the first store, which they could not pass
+    auto read = [&](int s, typename RawVec<X, 2>::T* rx, GR* rg) {
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             rx[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
             rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
         }
+    };
+    auto form = [&](int s, unsigned starts, int own, Held& hd) {
+        float h[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+        GR rg[TS];
+        read(s, hd.x, rg);
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             float xv[2], a[2];
-            unpack(rx[j], xv);
+            unpack(hd.x[j], xv);
             unpack(rg[j], a);
             scan_log2(a);
             add2(L, a, L);
             a[0] = scan_pow2(a[0]);
             a[1] = scan_pow2(a[1]);
-            if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
-            if (PACKED && (starts >> j & 1)) initial(t + j, h);
+            if constexpr (HELD) hd.a[j][0] = a[0], hd.a[j][1] = a[1];
+            else if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
+            if (PACKED && (starts >> j & 1)) initial(__shfl_sync(~0u, own, j), h);
             fma2(a, h, xv, h);
         }
         return PACKED && starts ? make_float4(-1.f, -1.f, h[0], h[1])
                                 : make_float4(run_decay(L[0]), run_decay(L[1]), h[0], h[1]);
     };
     // the same tokens again from what comes in, to the output
-    auto finish = [&](int t, int s, unsigned starts, unsigned ends) {
+    auto finish = [&](int t, int s, Held& hd, unsigned starts, unsigned ends, int own) {
+        GR rg[TS];
+        if (!HELD) read(s, hd.x, rg);
         const int left = min(TS, p.T - t);
         X* o = y;
-        typename RawVec<X, 2>::T rx[TS];
-        typename RawVec<G, 2>::T rg[TS];
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            rx[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
-            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
-        }
 #pragma unroll
         for (int j = 0; j < TS; ++j, o += p.y_st) {
             float xv[2], a[2];
-            unpack(rx[j], xv);
-            unpack(rg[j], a);
-            if constexpr (sizeof(G) == 2) {
-                scan_log2(a);
-                a[0] = scan_pow2(a[0]);
-                a[1] = scan_pow2(a[1]);
+            unpack(hd.x[j], xv);
+            if constexpr (HELD) {
+                a[0] = hd.a[j][0];
+                a[1] = hd.a[j][1];
+            } else {
+                unpack(rg[j], a);
+                if constexpr (sizeof(G) == 2) {
+                    scan_log2(a);
+                    a[0] = scan_pow2(a[0]);
+                    a[1] = scan_pow2(a[1]);
+                }
             }
-            if (PACKED && (starts >> j & 1)) initial(t + j, cin);
+            if (PACKED && (starts >> j & 1)) initial(__shfl_sync(~0u, own, j), cin);
             fma2(a, cin, xv, cin);
             if (live && j < left) scan_store<X, EVEN>(o, cin, live1);
-            if (PACKED && (ends >> j & 1) && live && p.fin) {
-                float* f = p.fin + scan_owner(p.cu, p.N, t + j) * p.fin_sn + c;
-                f[0] = cin[0];
-                if (live1) f[1] = cin[1];
+            if (PACKED && (ends >> j & 1)) {
+                float* f = p.fin + __shfl_sync(~0u, own, j) * p.fin_sn + c;
+                if (live && p.fin) {
+                    f[0] = cin[0];
+                    if (live1) f[1] = cin[1];
+                }
             }
         }
         // the places past the last token hold a = 1, x = 0: they leave h as it is
@@ -617,59 +645,76 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_piped(ScanParams 
             if (live1) p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
-    ScanSeq seq;
-    auto next = [&](int t, int s) {       // the run of a tile that has landed
+    ScanSeq<TS, 1> seq;
+    auto next = [&](int t, int s, Held& hd) {   // the run of a tile that has landed
         __syncwarp();
+        unsigned cut = 0;
         if (PACKED) {
-            seq.find<TS, 1>(p, t);
-            sm.warp[w][lane] = seq.starts ? form(t, s, seq.starts) : form(t, s, 0u);
-        } else {
-            sm.warp[w][lane] = form(t, s, 0u);
+            seq.find(p, t, p.s0, p.s0_sn, c);
+            cut = seq.starts;
         }
-        bar_arrive(kBarRuns, kScanPipedThreads);
+        sm.warp[w][lane] = PACKED && cut ? form(s, cut, seq.own, hd) : form(s, 0u, 0, hd);
+        bar_arrive(kBarRuns, kScanThreadsOf<HELD>);
+        if (HELD) {                              // its place is free
+            __syncwarp();
+            load(t + kScanStages * step, s);
+        }
     };
-    static_assert(kScanStages == 3, "the waits count the tiles behind the one wanted");
-    if (tiles > 0) {
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        next(t0, 0);
-    }
+    Held even, odd;
     int s = 0;
-    for (int i = 0; i < tiles; ++i, t0 += step, y += y_tile) {
-        bar_sync(kBarCin, kScanPipedThreads);
+    if (tiles > 0) {
+        cp_async_wait<kScanStages - 1>();
+        next(t0, 0, even);
+    }
+    auto tile = [&](int i, Held& now, Held& then) {
+        bar_sync(kBarCin, kScanThreadsOf<HELD>);
         const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
         cin[0] = in.x;
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
-        const int s1 = s + 1 == kScanStages ? 0 : s + 1;
+        const int own = seq.own, s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            next(t0 + step, s1);
+            cp_async_wait<HELD ? kScanStages - 1 : kScanStages - 2>();
+            next(t0 + step, s1, then);
         }
-        if (PACKED && (starts | ends)) finish(t0, s, starts, ends);
-        else finish(t0, s, 0u, 0u);
-        __syncwarp();
-        load(t0 + kScanStages * step, s);
+        if (PACKED && (starts | ends)) finish(t0, s, now, starts, ends, HELD ? own : seq.owner(p, t0));   // (registers, or a search)
+        else finish(t0, s, now, 0u, 0u, 0);
+        if (!HELD) {
+            __syncwarp();
+            load(t0 + kScanStages * step, s);
+        }
         s = s1;
+        t0 += step;
+        y += y_tile;
+    };
+    if constexpr (HELD) {
+        for (int i = 0; i < tiles; i += 2) {
+            tile(i, even, odd);
+            if (i + 1 < tiles) tile(i + 1, odd, even);
+        }
+    } else {
+        for (int i = 0; i < tiles; ++i) tile(i, even, odd);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     scan_leave<CL>();
 }
 
-template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN>
-__global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
+template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN, bool HELD>
+__global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    using Stage = ScanStage<X, G, TS, true>;       // then [2][K][32] float4: the CTAs' runs
+    constexpr int W = kScanWarps<HELD>;
+    using Stage = ScanStage<X, G, TS, true, W>;       // then [2][K][32] float4: the CTAs' runs
     Stage& st = *reinterpret_cast<Stage*>(dyn);
-    __shared__ ScanRuns sm;
+    __shared__ ScanRuns<W> sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
     const int b = item / ct, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (item % ct) * 64, c = c0 + lane * 2;
     const bool live = c < p.D, live1 = EVEN || c + 1 < p.D, whole = c0 + 64 <= p.D;
-    const int step = K * kScanWarps * TS;
+    const int step = K * W * TS;
     const int tiles = (int)(((int64_t)p.T + step - 1) / step);
-    int t0 = p.T - 1 - ((int)rank * kScanWarps + w) * TS;    // token of place j of tile i: t0 - j
+    int t0 = p.T - 1 - ((int)rank * W + w) * TS;    // token of place j of tile i: t0 - j
     ScanSrc<X, TS, -1, EVEN> ds(static_cast<const X*>(p.x) + b * p.x_sb, p.x_st, t0, step, c0, p.D, wide & 1);
     ScanSrc<G, TS, -1, EVEN> gs(static_cast<const G*>(p.g) + b * p.g_sb, p.g_st, t0, step, c0, p.D, wide & 2);
     ScanSrc<X, TS, -1, EVEN> hs(static_cast<const X*>(p.h) + b * p.h_sb, p.h_st, t0 - 1, step, c0, p.D, wide & 4);
@@ -680,27 +725,24 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         const bool inside = whole && t >= TS - 1;
         ds.copy(&st.x[s][w][0][0], t, p.T, inside);
         gs.copy(&st.g[s][w][0][0], t, p.T, inside);
+        hs.copy(&st.h[s][w][0][0], t - 1, p.T, inside && t >= TS);
+        cp_async_commit();
     };
-    auto load_h = [&](int t, int i) { hs.copy(&st.h[i & 1][w][0][0], t - 1, p.T, whole && t >= TS); };
-    if (w < kScanWarps)
+    if (w < W)
 #pragma unroll
-        for (int s = 0; s < kScanStages; ++s) {
-            load(t0 - s * step, s);
-            if (s < 2) load_h(t0 - s * step, s);
-            cp_async_commit();
-        }
+        for (int s = 0; s < kScanStages; ++s) load(t0 - s * step, s);
     if (PACKED) {
         scan_check_cu(p);
-        if (w < kScanWarps) scan_empty(p, p.sT, p.sT_sn, c, K, rank);
+        if (w < W) scan_empty<W>(p, p.sT, p.sT_sn, c, K, rank);
     }
-    scan_enter<CL>(sm);
-    if (w == kScanWarps) {
-        float carry[2] = {0.f, 0.f};
-        if (!PACKED && live && p.sT) {
-            carry[0] = p.sT[b * p.sT_sn + c];
-            if (live1) carry[1] = p.sT[b * p.sT_sn + c + 1];
-        }
-        scan_join<PACKED, CL>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
+    scan_enter<CL, W>(sm);
+    float cin[2], carry[2] = {0.f, 0.f};
+    if (!PACKED && live && p.sT) {
+        carry[0] = p.sT[b * p.sT_sn + c];
+        if (live1) carry[1] = p.sT[b * p.sT_sn + c + 1];
+    }
+    if (w == W) {
+        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
@@ -708,64 +750,79 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
         scan_leave<CL>();
         return;
     }
-    float cin[2];
     auto state = [&](const float* src, int64_t sn, int n, float* s) {
         s[0] = live && src ? src[n * sn + c] : 0.f;
         s[1] = live && live1 && src ? src[n * sn + c + 1] : 0.f;
     };
-    auto form = [&](int t, int s, unsigned ends) {
-        float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
-        typename RawVec<X, 2>::T rd[TS];
-        typename RawVec<G, 2>::T rg[TS];
+    using XR = typename RawVec<X, 2>::T;
+    using GR = typename RawVec<G, 2>::T;
+    struct Held {                              // the tokens of a run
+        XR d[TS], h[TS];
+        float a[TS][2];
+    };
+    auto read = [&](int s, XR* rd, GR* rg) {
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             rd[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
             rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
         }
+    };
+    auto read_h = [&](int s, XR* rh) {
+#pragma unroll
+        for (int j = 0; j < TS; ++j) rh[j] = ld_raw<X, 2>(&st.h[s][w][j][lane * 2]);
+    };
+    auto form = [&](int s, unsigned ends, int own, Held& hd) {
+        float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+        GR rg[TS];
+        read(s, hd.d, rg);
+        if (HELD) read_h(s, hd.h);
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             float dv[2], a[2];
-            unpack(rd[j], dv);
+            unpack(hd.d[j], dv);
             unpack(rg[j], a);
             scan_log2(a);
             add2(L, a, L);
             a[0] = scan_pow2(a[0]);
             a[1] = scan_pow2(a[1]);
-            if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
-            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, scan_owner(p.cu, p.N, t - j), e);
+            if constexpr (HELD) hd.a[j][0] = a[0], hd.a[j][1] = a[1];
+            else if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
+            if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, __shfl_sync(~0u, own, j), e);
             add2(dv, e, e);
             mul2(a, e, e);
         }
         return PACKED && ends ? make_float4(-1.f, -1.f, e[0], e[1])
                               : make_float4(run_decay(L[0]), run_decay(L[1]), e[0], e[1]);
     };
-    auto finish = [&](int t, int s, int hslot, unsigned starts, unsigned ends) {
+    auto finish = [&](int t, int s, Held& hd, unsigned starts, unsigned ends, int own) {
+        GR rg[TS];
+        if (!HELD) {
+            read(s, hd.d, rg);
+            read_h(s, hd.h);
+        }
         // places up to `left` hold tokens; dense: place left - 1 of the last tile is token 0
         const int left = max(0, min(TS, t + 1));
         const bool at0 = !PACKED && left > 0 && t < TS;
         X* ox = dx;
         G* og = dg;
-        typename RawVec<X, 2>::T rd[TS], rh[TS];
-        typename RawVec<G, 2>::T rg[TS];
-#pragma unroll
-        for (int j = 0; j < TS; ++j) {
-            rd[j] = ld_raw<X, 2>(&st.x[s][w][j][lane * 2]);
-            rg[j] = ld_raw<G, 2>(&st.g[s][w][j][lane * 2]);
-            rh[j] = ld_raw<X, 2>(&st.h[hslot][w][j][lane * 2]);
-        }
 #pragma unroll
         for (int j = 0; j < TS; ++j, ox -= p.y_st, og -= p.dg_st) {
             float dv[2], a[2], hv[2];
-            unpack(rd[j], dv);
-            unpack(rg[j], a);
-            unpack(rh[j], hv);
-            if constexpr (sizeof(G) == 2) {
-                scan_log2(a);
-                a[0] = scan_pow2(a[0]);
-                a[1] = scan_pow2(a[1]);
+            unpack(hd.d[j], dv);
+            unpack(hd.h[j], hv);
+            if constexpr (HELD) {
+                a[0] = hd.a[j][0];
+                a[1] = hd.a[j][1];
+            } else {
+                unpack(rg[j], a);
+                if constexpr (sizeof(G) == 2) {
+                    scan_log2(a);
+                    a[0] = scan_pow2(a[0]);
+                    a[1] = scan_pow2(a[1]);
+                }
             }
             int n = b;
-            if (PACKED && ((starts | ends) >> j & 1)) n = scan_owner(p.cu, p.N, t - j);
+            if (PACKED && ((starts | ends) >> j & 1)) n = __shfl_sync(~0u, own, j);
             if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, n, cin);
             if (PACKED ? (starts >> j & 1) : at0 && j == left - 1) state(p.s0, p.s0_sn, n, hv);
             float d[2], q[2];
@@ -787,40 +844,56 @@ __global__ void __launch_bounds__(kScanPipedThreads, 2) k_scan_bwd_piped(ScanPar
             if (live1) p.fin[b * p.fin_sn + c + 1] = cin[1];
         }
     };
-    ScanSeq seq;
-    auto next = [&](int t, int s) {
+    ScanSeq<TS, -1> seq;
+    auto next = [&](int t, int s, Held& hd) {   // the run of a tile that has landed
         __syncwarp();
+        unsigned cut = 0;
         if (PACKED) {
-            seq.find<TS, -1>(p, t);
-            sm.warp[w][lane] = seq.ends ? form(t, s, seq.ends) : form(t, s, 0u);
-        } else {
-            sm.warp[w][lane] = form(t, s, 0u);
+            seq.find(p, t, p.sT, p.sT_sn, c);
+            cut = seq.ends;
         }
-        bar_arrive(kBarRuns, kScanPipedThreads);
+        sm.warp[w][lane] = PACKED && cut ? form(s, cut, seq.own, hd) : form(s, 0u, 0, hd);
+        bar_arrive(kBarRuns, kScanThreadsOf<HELD>);
+        if (HELD) {                              // its place is free
+            __syncwarp();
+            load(t - kScanStages * step, s);
+        }
     };
-    if (tiles > 0) {
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        next(t0, 0);
-    }
+    Held even, odd;
     int s = 0;
-    for (int i = 0; i < tiles; ++i, t0 -= step, dx -= dx_tile, dg -= dg_tile) {
-        bar_sync(kBarCin, kScanPipedThreads);
+    if (tiles > 0) {
+        cp_async_wait<kScanStages - 1>();
+        next(t0, 0, even);
+    }
+    auto tile = [&](int i, Held& now, Held& then) {
+        bar_sync(kBarCin, kScanThreadsOf<HELD>);
         const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
         cin[0] = in.x;
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
-        const int s1 = s + 1 == kScanStages ? 0 : s + 1;
-        // x and g of tile i + 1 and h of tile i are there: the last tile waits for its h, too
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        if (i + 1 < tiles) next(t0 - step, s1);
-        else __syncwarp();
-        if (PACKED && (starts | ends)) finish(t0, s, i & 1, starts, ends);
-        else finish(t0, s, i & 1, 0u, 0u);
-        __syncwarp();
-        load(t0 - kScanStages * step, s);
-        load_h(t0 - 2 * step, i);
-        cp_async_commit();
+        const int own = seq.own, s1 = s + 1 == kScanStages ? 0 : s + 1;
+        if (i + 1 < tiles) {
+            cp_async_wait<HELD ? kScanStages - 1 : kScanStages - 2>();
+            next(t0 - step, s1, then);
+        }
+        if (PACKED && (starts | ends)) finish(t0, s, now, starts, ends, HELD ? own : seq.owner(p, t0));   // (registers, or a search)
+        else finish(t0, s, now, 0u, 0u, 0);
+        if (!HELD) {
+            __syncwarp();
+            load(t0 - kScanStages * step, s);
+        }
         s = s1;
+        t0 -= step;
+        dx -= dx_tile;
+        dg -= dg_tile;
+    };
+    if constexpr (HELD) {
+        for (int i = 0; i < tiles; i += 2) {
+            tile(i, even, odd);
+            if (i + 1 < tiles) tile(i + 1, odd, even);
+        }
+    } else {
+        for (int i = 0; i < tiles; ++i) tile(i, even, odd);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     scan_leave<CL>();
