@@ -2,7 +2,8 @@
 
 Argument marshalling only: torch tensors are described as ``dn_tensor``
 structs (pointer, dtype, shape, strides in elements) and handed to the shared
-library.  Every step of the computation runs in the library's CUDA kernels;
+library (the operators around the mixers by csrc/dn_call.cpp, where the call is
+a plain one).  Every step of the computation runs in the library's CUDA kernels;
 there is no other implementation to fall back to.  If the library is missing
 or cannot be loaded, every call raises.
 """
@@ -10,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
@@ -424,6 +427,31 @@ def _descriptors(*tensors):
     return addr
 
 
+_call = None
+
+
+def _short():
+    """The calls that need no marshalling here (csrc/dn_call.cpp): each takes its binding's
+    arguments and answers None where they want the general way below."""
+    global _call
+    if _call is None:
+        load()
+        if not os.path.exists(_build.CALL):
+            raise RuntimeError(f"{_build.CALL} not found; run "
+                               "`python -m deltanet_chunkwise_delta_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("dn_call", _build.CALL)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dn_call", loader))
+        loader.exec_module(module)
+        _call = module
+    return _call
+
+
+def _answer(r):
+    if type(r) is int:
+        _check(r)
+    return r
+
+
 _HERE = contextlib.nullcontext()
 # The current stream's handle without a Stream object around it, where torch offers it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -469,6 +497,10 @@ def deltanet_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch
     state [M, H, d_k, d_v] fp32; slot_idx int32 [N] names each request's row of it (-1: a
     padding request, whose rows of out are zero), None: request n uses row n.  Returns out
     [N, T, H, d_v].  Asynchronous on ``stream`` (default: torch's current stream)."""
+    if stream is None:
+        r = (_call or _short()).step(q, k, v, beta, state, g, n_h, slot_idx, out)
+        if r is not None:
+            return _answer(r)
     handle, here = _place("deltanet_step", stream, q, k, v, beta, state, g, slot_idx, out)
     with here:
         if out is None:
@@ -490,6 +522,11 @@ def deltanet_scan_fwd(x: torch.Tensor, g: torch.Tensor,
     initial_state [N, D] fp32 or None; cu_seqlens int32 [N+1] or None.  Returns (out,
     final_state or None): every h_t in the dtype of x and the last one of each sequence
     in fp32."""
+    if stream is None:
+        r = (_call or _short()).scan_fwd(x, g, initial_state, cu_seqlens, out, final_state,
+                                         output_final_state)
+        if r is not None:
+            return _answer(r)
     handle, here = _place("deltanet_scan_fwd", stream, x, g, initial_state, cu_seqlens, out, final_state)
     with here:
         if out is None:
@@ -511,6 +548,11 @@ def deltanet_scan_bwd(g: torch.Tensor, out: torch.Tensor, d_out: torch.Tensor,
     """Gradients of ``deltanet_scan_fwd`` from its output ``out``: (d_x, d_g,
     d_initial_state), the last where initial_state (or a buffer for it) is given, else
     None.  d_final_state [N, D] fp32, or None for zeros."""
+    if stream is None:
+        r = (_call or _short()).scan_bwd(g, out, d_out, initial_state, cu_seqlens, d_final_state,
+                                         d_x, d_g, d_initial_state)
+        if r is not None:
+            return _answer(r)
     handle, here = _place("deltanet_scan_bwd", stream, g, out, d_out, initial_state, cu_seqlens,
                           d_final_state, d_x, d_g, d_initial_state)
     with here:
@@ -532,6 +574,10 @@ def deltanet_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     """The gated linear recurrence for the few tokens of a decoding step: x, g [N, T, D],
     state [M, D] fp32 updated in place, slot_idx as ``deltanet_step``.  Returns out
     [N, T, D]."""
+    if stream is None:
+        r = (_call or _short()).scan_step(x, g, state, slot_idx, out)
+        if r is not None:
+            return _answer(r)
     handle, here = _place("deltanet_scan_step", stream, x, g, state, slot_idx, out)
     with here:
         if out is None:
@@ -566,6 +612,11 @@ def deltanet_norm_fwd(y: torch.Tensor, weight: Optional[torch.Tensor] = None,
     residual_out): without residual (y2, None); with it (n, r'), n None without
     next_weight."""
     act = _activation(activation)
+    if stream is None:
+        r = (_call or _short()).norm_fwd(y, weight, gate, residual, scale, next_weight, act, eps,
+                                         out, residual_out)
+        if r is not None:
+            return _answer(r)
     handle, here = _place("deltanet_norm_fwd", stream, y, weight, gate, residual, scale, next_weight,
                           out, residual_out)
     with here:
@@ -602,6 +653,11 @@ def deltanet_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor],
     where the forward call has no out) and d_residual_out of residual_out (None: zeros,
     where next_weight is given).  Buffers for the row gradients may be passed in."""
     act = _activation(activation)
+    if stream is None:
+        r = (_call or _short()).norm_bwd(y, d_out, weight, gate, residual, scale, next_weight,
+                                         d_residual_out, act, eps, d_y, d_gate, d_residual)
+        if r is not None:
+            return NormGrads._make(_answer(r))
     handle, here = _place("deltanet_norm_bwd", stream, y, d_out, weight, gate, residual, scale,
                           next_weight, d_residual_out, d_y, d_gate, d_residual)
     with here:

@@ -2,20 +2,24 @@
 
 ``python -m deltanet_chunkwise_delta_b200.build`` compiles the ``csrc/*.cu``
 files with nvcc into ``_build/libdeltanet_b200.so`` inside the package directory, so
-the library travels with the source tree.
+the library travels with the source tree, and ``csrc/dn_call.cpp``, the binding's short
+way to it, with g++ into ``_build/dn_call.so`` beside it.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", name)
         for name in ("deltanet.cu", "deltanet_noalloc.cu", "deltanet_ops.cu", "deltanet_norm.cu")]
 LIB = os.path.join(PKG, "_build", "libdeltanet_b200.so")
+CALL = os.path.join(PKG, "_build", "dn_call.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -32,10 +36,33 @@ def _sources():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return any(os.path.getmtime(s) > t for s in _sources())
+
+
+def _run(cmd, verbose):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed:\n" + res.stdout + res.stderr)
+    if verbose:
+        sys.stderr.write(res.stderr)
+    return res.stderr
+
+
+def _build_call(verbose: bool) -> None:
+    """The binding's short way: linked to the library beside it and to torch's own."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = CALL + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+          "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(cuda, "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-o", tmp,
+          os.path.join(PKG, "csrc", "dn_call.cpp"), "-L" + os.path.dirname(LIB),
+          "-l:" + os.path.basename(LIB), "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
+          "-ltorch", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, CALL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -45,15 +72,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, *SRCS]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
-    if verbose:
-        sys.stderr.write(res.stderr)
+    err = _run(cmd, verbose)
     log = os.path.join(os.path.dirname(LIB), "ptxas.log")
     with open(log, "w") as f:
-        f.write(res.stderr)
+        f.write(err)
     os.replace(tmp, LIB)
+    _build_call(verbose)
     return LIB
 
 

@@ -223,5 +223,15 @@ def test_descriptor_bytes_are_the_struct():
         L._descriptors(torch.zeros(2, dtype=torch.float16))
 
 
+def test_short_calls_leave_cpu_tensors_to_the_general_way(lib):
+    c = L._short()
+    t = torch.zeros(2, 3, 4)
+    assert c.scan_step(t, t, t[0], None, None) is None
+    assert c.norm_fwd(t, None, None, None, None, None, 0, 1e-6, None, None) is None
+    assert c.scan_fwd(None, t, None, None, None, None, True) is None
+    with pytest.raises(TypeError):
+        c.step(t)
+
+
 def test_status_string_of_slots():
     assert L.status_string(L.DN_ERR_SLOTS).startswith("DN_ERR_SLOTS")
