@@ -23,17 +23,18 @@ bool scalars_ok(const dn_tensor* t, const int64_t* dims) {
     return numel(t) == 0 || (t->data && reinterpret_cast<uintptr_t>(t->data) % 4 == 0);
 }
 
-template <typename E, int DK, int DV, bool ONE>
+template <typename E, int DK, int DV, StepKind KIND>
 void launch_step(const StepParams& p, int gate, unsigned grid, cudaStream_t s) {
-    if (gate == 0) k_step<E, DK, DV, 0, ONE><<<grid, DK, 0, s>>>(p);
-    else if (gate == 1) k_step<E, DK, DV, 1, ONE><<<grid, DK, 0, s>>>(p);
-    else k_step<E, DK, DV, 2, ONE><<<grid, DK, 0, s>>>(p);
+    if (gate == 0) k_step<E, DK, DV, 0, KIND><<<grid, DK, 0, s>>>(p);
+    else if (gate == 1) k_step<E, DK, DV, 1, KIND><<<grid, DK, 0, s>>>(p);
+    else k_step<E, DK, DV, 2, KIND><<<grid, DK, 0, s>>>(p);
 }
 
 template <typename E, int DK, int DV>
 void launch_step(const StepParams& p, int gate, unsigned grid, cudaStream_t s) {
-    if (p.T == 1 && p.nh == 1) launch_step<E, DK, DV, true>(p, gate, grid, s);
-    else launch_step<E, DK, DV, false>(p, gate, grid, s);
+    if (p.nh > 1) launch_step<E, DK, DV, kStepWrites>(p, gate, grid, s);
+    else if (p.T > 1) launch_step<E, DK, DV, kStepTokens>(p, gate, grid, s);
+    else launch_step<E, DK, DV, kStepOne>(p, gate, grid, s);
 }
 
 template <typename E>
