@@ -322,8 +322,18 @@ dn_status deltanet_norm_bwd(const dn_tensor* y, const dn_tensor* weight, const d
     }
     if (sums) {
         auto f = [](dn_tensor* t) { return t ? static_cast<float*>(t->data) : nullptr; };
-        k_norm_bwd_sum<<<dim3((unsigned)((d + 31) / 32), 3), 256, 0, stream>>>(
-            p.part, ctas, (int)d, f(d_weight), f(d_scale), f(d_next_weight));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((d + 31) / 32), 3);
+        cfg.blockDim = dim3(32 * kNormSumGroups);
+        cfg.stream = stream;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = p.rows > 0;
+        if (cudaLaunchKernelEx(&cfg, k_norm_bwd_sum, (const float*)p.part, ctas, (int)d, f(d_weight), f(d_scale),
+                               f(d_next_weight)) != cudaSuccess)
+            return DN_ERR_CUDA;
         ++launches;
     }
     return launched(launches);

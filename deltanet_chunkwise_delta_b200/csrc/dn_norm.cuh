@@ -96,8 +96,8 @@ __device__ __forceinline__ float norm_act(float z, int act, float* grad = nullpt
 // 16384 rows of 2049 bf16 elements forward with gate and residual 151 us, 250 read one by one.
 //
 // B200, 16384 rows of 2048: residual sum and next norm 66 us (93 % of the measured copy rate),
-// the whole chain backward 120 us (68 %: 55 % of the issue slots in use, all that the warps of
-// two CTAs give); 262144 heads of 128: gated norm 37 us (83 %), backward 64 us (80 %).
+// the whole chain backward 118 us (69 %: 55 % of the issue slots in use, all that the warps of
+// two CTAs give); 262144 heads of 128: gated norm 37 us (83 %), backward 60 us (85 %).
 
 template <int TPR>
 constexpr int kNormCta = TPR == 0 ? 320 : TPR == 1 ? 512 : TPR <= 32 ? kNormThreads : TPR;
@@ -572,6 +572,7 @@ __global__ void __launch_bounds__(kNormCta<TPR>, TPR <= 1 || TPR == 512 ? 1 : TP
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!p.part) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // this CTA's partial sums: its groups of rows in order
     float* sums = p.part + (int64_t)blockIdx.x * 3 * d;
     auto put = [&](int k, const float* acc) {
@@ -814,6 +815,7 @@ __global__ void __launch_bounds__(kNormLong) k_norm_bwd_long(NormParams p) {
         }
     }
     if (!p.part) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float* sums = p.part + (int64_t)blockIdx.x * 3 * p.d;
     for (int k = 0; k < 3; ++k)
         for (int i = 0; i < pieces; ++i) {
@@ -827,23 +829,34 @@ __global__ void __launch_bounds__(kNormLong) k_norm_bwd_long(NormParams p) {
         }
 }
 
-// d_weight, d_scale, d_next_weight from the partial sums of G CTAs: 32 columns per CTA, 8
-// groups of partials each added in order, then the groups in order.
-__global__ void __launch_bounds__(256) k_norm_bwd_sum(const float* part, int G, int d, float* dw,
-                                                      float* ds, float* dn) {
-    __shared__ float sh[8][32];
+// d_weight, d_scale, d_next_weight from the partial sums of G CTAs: 32 columns per CTA, 32
+// groups of partials each added in order, then the groups in order.  A thread's partials are
+// all on their way at once, and the CTAs start with the end of the rows' kernel and wait for
+// what it wrote (8 groups, one partial after another, after that kernel: the heads' backward
+// took 63 us, not 60).
+constexpr int kNormSumGroups = 32;
+__global__ void __launch_bounds__(32 * kNormSumGroups) k_norm_bwd_sum(const float* part, int G, int d, float* dw,
+                                                                       float* ds, float* dn) {
+    constexpr int PER = (kNormBwdCtas + kNormSumGroups - 1) / kNormSumGroups;
+    __shared__ float sh[kNormSumGroups][33];
     float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dn;
     if (!out) return;
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (j < d)
-        for (int i = grp; i < G; i += 8) s += part[((int64_t)i * 3 + blockIdx.y) * d + j];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float v[PER], s = 0.f;
+#pragma unroll
+    for (int n = 0; n < PER; ++n) {
+        const int i = grp + n * kNormSumGroups;
+        v[n] = j < d && i < G ? part[((int64_t)i * 3 + blockIdx.y) * d + j] : 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < PER; ++n) s += v[n];
     sh[grp][lane] = s;
     __syncthreads();
     if (grp == 0 && j < d) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += sh[i][lane];
+        for (int i = 0; i < kNormSumGroups; ++i) t += sh[i][lane];
         out[j] = t;
     }
 }
