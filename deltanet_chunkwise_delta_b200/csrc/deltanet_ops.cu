@@ -164,9 +164,10 @@ dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     constexpr bool H1 = !BWD && sizeof(G) == 2, HK = !BWD;
     constexpr int T1 = sizeof(X) == 4 ? 4 : 8, TK = T1 + (HK && EVEN ? 4 : 0);
     constexpr int W1 = kScanWarps<H1>, WK = kScanWarps<HK>;
-    constexpr int stage = (int)sizeof(ScanStage<X, G, T1, BWD, W1>), part = (int)sizeof(ScanStage<X, G, TK, BWD, WK>);
-    static_assert(2 * (stage + sizeof(ScanRuns<W1>) + 1024) <= 228 * 1024 &&
-                  2 * (part + 8192 + sizeof(ScanRuns<WK>) + 1024) <= 228 * 1024, "two CTAs on an SM, clusters of 8");
+    constexpr int stage = kScanPlace<BWD> + (int)sizeof(ScanStage<X, G, T1, BWD, W1>);
+    constexpr int part = kScanPlace<BWD> + (int)sizeof(ScanStage<X, G, TK, BWD, WK>);
+    static_assert(2 * (stage + sizeof(ScanRuns<W1, false>) + 128 + 1024) <= 228 * 1024 &&
+                  2 * (part + 8192 + sizeof(ScanRuns<WK, true>) + 128 + 1024) <= 228 * 1024, "two CTAs on an SM, clusters of 8");
     const int K = scan_cluster(items, p.T, WK * TK, sms);
     const int wide = scan_wide(p, sizeof(X) == 4 ? DN_F32 : DN_BF16, sizeof(G) == 4 ? DN_F32 : DN_BF16);
     if (items > kMax31 / K) return DN_ERR_INVALID_ARG;

@@ -2,6 +2,8 @@
 // channel by channel, and its gradients.
 #pragma once
 
+#include <type_traits>
+
 #include "dn_common.cuh"
 #include "dn_sm100.cuh"
 #include "dn_step.cuh"
@@ -174,9 +176,13 @@ __global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) 
 // element is read once and written once.  Backward walks the tokens from the last one, with
 // c = a_t delta_t (what reaches token t - 1) in the place of h.
 //
+// A is formed from the sum of its logarithms (run_factor): the product of a run's decays may
+// pass what fp32 holds either way where h does not.
+//
 // Packed input: the run's map is cut where a sequence starts (backward: ends).  Such a run
 // passes H on whatever comes in, so that nothing of another sequence, NaN included, leaks:
-// A = -1 marks it (products of decays are >= 0).
+// a logarithm of NaN marks it, which its sums with others keep (where it is the decays' own,
+// H is NaN as well).
 //
 // The tokens come through shared memory (cp.async; a warp reads only what it copied itself).
 // The warps form the (A, H) of tile i + 1 before they finish tile i; one more warp joins the
@@ -211,17 +217,23 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// carry <- A carry + H (H alone where A is the mark)
-template <bool PACKED>
-__device__ __forceinline__ float run_map(float A, float H, float carry) {
-    const float x = fmaf(A, carry, H);
-    return PACKED && A < 0.f ? H : x;
+// The product A of a run's decays from its logarithm l (base 2): A where fp32 holds it with room
+// (|l| <= 126), else -2^(l/3), which stands for three steps c -> 2^(l/3) c.  They go the same way,
+// so nothing overflows or vanishes ahead of A c, whatever finite c makes A c finite (one factor
+// would end at 2^128, far from what a tiny c may grow by).  Below 2^-252 A c is less than 2^-124:
+// 0.  NaN stays NaN.
+__device__ __forceinline__ float run_factor(float l) {
+    const bool near = fabsf(l) <= 126.f;
+    const float r = scan_pow2(near ? l : l > 381.f ? 127.f : l * 0.333333343f);
+    return near ? r : l < -252.f ? 0.f : -r;
 }
-// The product of two runs' decays.  Kept below infinity, so that a growing run still maps 0 to H.
-template <bool PACKED>
-__device__ __forceinline__ float run_prod(float A, float B) {
-    const float x = fminf(A * B, 3.402823466e38f);
-    return PACKED && (A < 0.f || B < 0.f) ? -1.f : x;
+// carry <- A carry + H (H alone where A is the mark).  FAR: f is the run_factor of A, not A.
+template <bool PACKED, bool FAR>
+__device__ __forceinline__ float run_map(float f, float H, float carry) {
+    float x = carry;
+    if (FAR && f < 0.f) x = f * (f * x), f = -f;
+    x = fmaf(f, x, H);
+    return PACKED && f != f ? H : x;
 }
 
 // Packed input: state rows of sequences without tokens (forward: final = initial state;
@@ -339,26 +351,37 @@ __device__ __forceinline__ void scan_store(E* q, const float* f, bool second) {
 
 // A warp's run of tile i + 1 is written after it has read what comes into that of tile i: one
 // place.  The other CTAs may be a tile ahead: theirs go by tile parity.
-template <int W>
+template <int W, bool CL>
 struct ScanRuns {
     float4 warp[W][32];                   // (A0, A1, H0, H1) of each warp's run; then, in its
                                           // first half, what comes into the run
+    float2 logs[W][32];                   // the logarithms of A0, A1
     uint64_t full[2];                     // the cluster's runs of a tile have arrived
+    // A where it is one factor, in a cluster together with the CTA's other runs; else infinite
+    static __device__ __forceinline__ float factor(float l) {
+        return fabsf(l) > (CL ? 126.f / 8 : 126.f) ? __uint_as_float(0x7f800000u) : scan_pow2(l);
+    }
+    // h and the logarithms of one warp's run; cut: it passes on h alone
+    __device__ __forceinline__ void put(int w, float* l, const float* h, bool cut) {
+        const int lane = threadIdx.x & 31;
+        if (cut) l[0] = l[1] = __uint_as_float(0x7fffffffu);
+        logs[w][lane] = make_float2(l[0], l[1]);
+        warp[w][lane] = make_float4(factor(l[0]), factor(l[1]), h[0], h[1]);
+    }
+    static __device__ __forceinline__ bool is_far(float4 run) {
+        return run.x == __uint_as_float(0x7f800000u) || run.y == __uint_as_float(0x7f800000u);
+    }
+    // a run with factors that run_map<.., true> takes
+    __device__ __forceinline__ float4 farther(int w, float4 run) const {
+        const float2 l = logs[w][threadIdx.x & 31];
+        return make_float4(run_factor(l.x), run_factor(l.y), run.z, run.w);
+    }
 };
 
-// The product of a run's decays from the sum of their logarithms (base 2), kept below infinity.
-__device__ __forceinline__ float run_decay(float l) { return scan_pow2(fminf(l, 127.f)); }
-
-template <bool PACKED>
+template <bool PACKED, bool FAR>
 __device__ __forceinline__ void run_through(float4 r, float& c0, float& c1) {
-    c0 = run_map<PACKED>(r.x, r.z, c0);
-    c1 = run_map<PACKED>(r.y, r.w, c1);
-}
-// r after q
-template <bool PACKED>
-__device__ __forceinline__ float4 run_join(float4 r, float4 q) {
-    return make_float4(run_prod<PACKED>(r.x, q.x), run_prod<PACKED>(r.y, q.y), run_map<PACKED>(r.x, r.z, q.z),
-                       run_map<PACKED>(r.y, r.w, q.w));
+    c0 = run_map<PACKED, FAR>(r.x, r.z, c0);
+    c1 = run_map<PACKED, FAR>(r.y, r.w, c1);
 }
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -387,25 +410,52 @@ __device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity
 // The last warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
 // into the first tile, in the end what leaves the last one.
 template <bool PACKED, bool CL, int W>
-__device__ __forceinline__ void scan_join(ScanRuns<W>& sm, float4* cta, int tiles, int K, unsigned rank, float* carry, int* err) {
+__device__ __forceinline__ void scan_join(ScanRuns<W, CL>& sm, float4* cta, int tiles, int K,
+                                          unsigned rank, float* carry, int* err) {
     const int lane = threadIdx.x & 31;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
         const int par = i & 1;
         bar_sync(kBarRuns, (W + 1) * 32);
-        if constexpr (!CL) {
+        float4 run[W];
+        bool far = false;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float4 run = sm.warp[w][lane];
-                *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(carry[0], carry[1]);
-                run_through<PACKED>(run, carry[0], carry[1]);
-            }
+        for (int w = 0; w < W; ++w) far |= sm.is_far(run[w] = sm.warp[w][lane]);
+        if constexpr (!CL) {
+            auto through = [&](auto any) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float4 r = decltype(any)::value ? sm.farther(w, run[w]) : run[w];
+                    *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(carry[0], carry[1]);
+                    run_through<PACKED, decltype(any)::value>(r, carry[0], carry[1]);
+                }
+            };
+            if (far) through(std::true_type());
+            else through(std::false_type());
         } else {
+            // the runs ahead of each warp's as one map.  The product of their factors where that is
+            // one factor as well; else from the sum of their logarithms, which the chain over the
+            // warps would wait for (in every tile: 65536 x 512 a tenth longer).
             float4 pre[W], all = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 pre[w] = all;
-                all = run_join<PACKED>(sm.warp[w][lane], all);
+                all.x *= run[w].x;
+                all.y *= run[w].y;
+                run_through<PACKED, false>(run[w], all.z, all.w);
+            }
+            if (far) {
+                all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    pre[w] = make_float4(run_factor(all.x), run_factor(all.y), all.z, all.w);
+                    const float4 r = sm.farther(w, sm.warp[w][lane]);
+                    all.x += sm.logs[w][lane].x;
+                    all.y += sm.logs[w][lane].y;
+                    run_through<PACKED, true>(r, all.z, all.w);
+                }
+                all.x = run_factor(all.x);
+                all.y = run_factor(all.y);
             }
             if (lane == 0) sm100::mbar_expect_tx(&sm.full[par], K * 512);
             const uint32_t dst = sm100::saddr(cta + (par * K + rank) * 32 + lane), bar = sm100::saddr(&sm.full[par]);
@@ -423,16 +473,31 @@ __device__ __forceinline__ void scan_join(ScanRuns<W>& sm, float4* cta, int tile
             // without the others' runs nothing after them is known: NaN, not numbers of some kind
             if (!ok) carry[0] = carry[1] = __uint_as_float(0x7fffffffu);
             float c0 = 0.f, c1 = 0.f;
+            const float before[2] = {carry[0], carry[1]};
+            bool again = false;
             for (int r = 0; r < K; ++r) {
                 if (r == (int)rank) c0 = carry[0], c1 = carry[1];
-                run_through<PACKED>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
+                const float4 run = cta[(par * K + r) * 32 + lane];
+                again |= run.x < 0.f || run.y < 0.f;
+                run_through<PACKED, false>(run, carry[0], carry[1]);
             }
+            if (again) {
+                carry[0] = before[0], carry[1] = before[1];
+                for (int r = 0; r < K; ++r) {
+                    if (r == (int)rank) c0 = carry[0], c1 = carry[1];
+                    run_through<PACKED, true>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
+                }
+            }
+            auto into = [&](auto any) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                float x0 = c0, x1 = c1;
-                run_through<PACKED>(pre[w], x0, x1);
-                *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
-            }
+                for (int w = 0; w < W; ++w) {
+                    float x0 = c0, x1 = c1;
+                    run_through<PACKED, decltype(any)::value>(pre[w], x0, x1);
+                    *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
+                }
+            };
+            if (far) into(std::true_type());
+            else into(std::false_type());
         }
         bar_arrive(kBarCin, (W + 1) * 32);
     }
@@ -442,7 +507,7 @@ __device__ __forceinline__ void scan_join(ScanRuns<W>& sm, float4* cta, int tile
 // Before and after the work of a CTA of a cluster: barriers of the exchange ready everywhere,
 // nobody's memory gone while another CTA may still write to it.
 template <bool CL, int W>
-__device__ __forceinline__ void scan_enter(ScanRuns<W>& sm) {
+__device__ __forceinline__ void scan_enter(ScanRuns<W, CL>& sm) {
     if (CL && threadIdx.x == 0) {
         sm100::mbar_init(&sm.full[0], 1);
         sm100::mbar_init(&sm.full[1], 1);
@@ -512,6 +577,14 @@ struct ScanSeq {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Where they begin in shared memory, past a multiple of 128 bytes.  Forward on one: at 16 its
+// copies and reads take longer (8 x 2048 x 2048 51 us, not 45, packed 222459 x 2048 597, not 551,
+// 65536 x 512 118, not 102).  Backward at 16: long wide rows' five streams then come through
+// faster than at 0 (65536 x 2048 338 and 360 us, 2 x 8192 x 2048 88 and 96; 32768 x 1024, the
+// other way, 154 and 125).
+template <bool BWD>
+constexpr int kScanPlace = BWD ? 16 : 0;
+
 // The tokens on their way, a warp's rows together.
 template <typename X, typename G, int TS, bool BWD, int W>
 struct ScanStage {
@@ -522,11 +595,11 @@ struct ScanStage {
 
 template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN, bool HELD>
 __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanParams p, int K, int wide) {
-    extern __shared__ __align__(16) unsigned char dyn[];
+    extern __shared__ __align__(128) unsigned char dyn[];
     constexpr int W = kScanWarps<HELD>;
     using Stage = ScanStage<X, G, TS, false, W>;       // then [2][K][32] float4: the CTAs' runs
-    Stage& st = *reinterpret_cast<Stage*>(dyn);
-    __shared__ ScanRuns<W> sm;
+    Stage& st = *reinterpret_cast<Stage*>(dyn + kScanPlace<false>);
+    __shared__ ScanRuns<W, CL> sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
@@ -560,7 +633,7 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
         if (live1) carry[1] = p.s0[b * p.s0_sn + c + 1];
     }
     if (w == W) {
-        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
@@ -604,8 +677,7 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
             if (PACKED && (starts >> j & 1)) initial(__shfl_sync(~0u, own, j), h);
             fma2(a, h, xv, h);
         }
-        return PACKED && starts ? make_float4(-1.f, -1.f, h[0], h[1])
-                                : make_float4(run_decay(L[0]), run_decay(L[1]), h[0], h[1]);
+        sm.put(w, L, h, PACKED && starts);
     };
     // the same tokens again from what comes in, to the output
     auto finish = [&](int t, int s, Held& hd, unsigned starts, unsigned ends, int own) {
@@ -653,7 +725,8 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
             seq.find(p, t, p.s0, p.s0_sn, c);
             cut = seq.starts;
         }
-        sm.warp[w][lane] = PACKED && cut ? form(s, cut, seq.own, hd) : form(s, 0u, 0, hd);
+        if (PACKED && cut) form(s, cut, seq.own, hd);
+        else form(s, 0u, 0, hd);
         bar_arrive(kBarRuns, kScanThreadsOf<HELD>);
         if (HELD) {                              // its place is free
             __syncwarp();
@@ -701,11 +774,11 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
 
 template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN, bool HELD>
 __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
-    extern __shared__ __align__(16) unsigned char dyn[];
+    extern __shared__ __align__(128) unsigned char dyn[];
     constexpr int W = kScanWarps<HELD>;
     using Stage = ScanStage<X, G, TS, true, W>;       // then [2][K][32] float4: the CTAs' runs
-    Stage& st = *reinterpret_cast<Stage*>(dyn);
-    __shared__ ScanRuns<W> sm;
+    Stage& st = *reinterpret_cast<Stage*>(dyn + kScanPlace<true>);
+    __shared__ ScanRuns<W, CL> sm;
     if (!CL) K = 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int item = blockIdx.x / K, ct = (p.D + 63) / 64;
@@ -742,7 +815,7 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
         if (live1) carry[1] = p.sT[b * p.sT_sn + c + 1];
     }
     if (w == W) {
-        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(dyn + sizeof(Stage)), tiles, K, rank, carry, p.err);
+        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p.err);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
@@ -791,8 +864,7 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
             add2(dv, e, e);
             mul2(a, e, e);
         }
-        return PACKED && ends ? make_float4(-1.f, -1.f, e[0], e[1])
-                              : make_float4(run_decay(L[0]), run_decay(L[1]), e[0], e[1]);
+        sm.put(w, L, e, PACKED && ends);
     };
     auto finish = [&](int t, int s, Held& hd, unsigned starts, unsigned ends, int own) {
         GR rg[TS];
@@ -852,7 +924,8 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
             seq.find(p, t, p.sT, p.sT_sn, c);
             cut = seq.ends;
         }
-        sm.warp[w][lane] = PACKED && cut ? form(s, cut, seq.own, hd) : form(s, 0u, 0, hd);
+        if (PACKED && cut) form(s, cut, seq.own, hd);
+        else form(s, 0u, 0, hd);
         bar_arrive(kBarRuns, kScanThreadsOf<HELD>);
         if (HELD) {                              // its place is free
             __syncwarp();

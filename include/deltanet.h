@@ -343,8 +343,10 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
  *
  * (the recurrence that the matrix-state forms run on each entry of their state,
  * here with a decay and an input per channel).  A run of tokens is the map
- * h -> A h + H with A the product of its decays; runs compose exactly, which is how
- * a sequence is split across warps and CTAs.
+ * h -> A h + H with A the product of its decays, which is how a sequence is split
+ * across warps and CTAs.  A is formed from the sum of its logarithms, so it may pass
+ * what fp32 holds, up or down, where h does not; H, what a run of up to 84 tokens adds
+ * up to by itself, has to stay in range as h does.  A h below 2^-124 may come out as 0.
  *
  *   x             [B, T, D]   bf16 or fp32
  *   g             [B, T, D]   fp32, or bf16 with bf16 x: ln a.  Any value but NaN and
