@@ -59,6 +59,8 @@ void by_types(int32_t x, int32_t g, F f) {
     else f(__nv_bfloat16(), __nv_bfloat16());
 }
 
+constexpr int64_t kMaxSize = kMax31 - 16384;
+
 // Shapes of deltanet_scan_fwd / _bwd: x [B, T, D] (x: its dtype and shape lead), g, the state
 // tensors, the packed boundaries.  Sets N.
 dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* cu, int64_t& N) {
@@ -66,7 +68,8 @@ dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* c
     const int64_t B = x->shape[0], T = x->shape[1], D = x->shape[2];
     if (B < 0 || T < 0 || D < 1 || D > kMax31 || T > kMax31 || B > kMax31) return DN_ERR_INVALID_ARG;
     if (T > 0 && B > kMax31 / T) return DN_ERR_INVALID_ARG;
-    if (T > kMax31 - 16384) return DN_ERR_INVALID_ARG;   // the kernels' token counters run past T by a few tiles
+    // the kernels' token counters run past T by a few tiles, their channels past D by a CTA's
+    if (T > kMaxSize || D > kMaxSize) return DN_ERR_INVALID_ARG;
     const int64_t dims[3] = {B, T, D};
     if (!view_ok(x, 3, dims, kF32 | kBf16)) return DN_ERR_INVALID_ARG;
     if (!view_ok(g, 3, dims, x->dtype == DN_F32 ? kF32 : kF32 | kBf16)) return DN_ERR_INVALID_ARG;

@@ -282,7 +282,7 @@ struct ScanSrc {
         constexpr int es = sizeof(E);
         row = wide ? lane / kPer : 0;
         const int c = c0 + (wide ? lane % kPer * (16 / es) : EVEN ? lane * 2 : lane);
-        const int bytes = (D - c) * es;
+        const int bytes = min(D - c, 64) * es;             // (a row may have more than 2^31)
         left = max(0, wide ? min(16, bytes) : EVEN ? min(2 * es, bytes) : bytes);
         base = p;
         cur = p + c + (t + DIR * row) * st;

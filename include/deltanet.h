@@ -357,7 +357,7 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
  *   final_state   [N, D] fp32 (the unrounded h after the last token; initial_state
  *                 for a sequence without tokens), or NULL
  *
- * D is any size >= 1; the last stride of every tensor is 1, other strides are any
+ * 1 <= D <= 2^31 - 16385, and T no larger; the last stride of every tensor is 1, other strides are any
  * non-negative numbers, data aligned to its element.  Aligned and even rows move in
  * wider pieces.  Outputs may be interleaved views of one buffer (rows side by side,
  * equal strides); any other overlap of an output is DN_ERR_ALIAS.  No workspace; with

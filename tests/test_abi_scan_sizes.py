@@ -1,0 +1,28 @@
+"""Sizes that deltanet_scan_* refuse before a GPU is touched: what the kernels' 32-bit counters of
+tokens and channels do not hold."""
+import pytest
+
+from deltanet_chunkwise_delta_b200 import _lib as L
+from deltanet_chunkwise_delta_b200 import build as B
+from tests.test_abi_block_ops import desc, ref
+
+MOST = 2 ** 31 - 16385
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return L.load()
+
+
+@pytest.mark.parametrize("T,D", [(1, MOST + 1), (1, 2 ** 31 - 1), (17, MOST + 1), (MOST + 1, 1), (1, 2 ** 31)])
+def test_rows_past_the_counters(lib, T, D):
+    # made-up addresses far enough apart for the sizes: what refuses is the size
+    at = lambda i, *s, t=L.DN_BF16: desc(list(s), t, 1 + i * 2 ** 10)
+    x, g, out = at(0, 1, T, D), at(1, 1, T, D), at(2, 1, T, D)
+    state, fin = at(3, 1, D, t=L.DN_F32), at(4, 1, D, t=L.DN_F32)
+    more = [at(5, 1, T, D), at(6, 1, T, D)]
+    args = lambda *a: [None if x is None else ref(x) for x in a] + [None]
+    assert lib.deltanet_scan_fwd(*args(x, g, None, None, out, fin)) == L.DN_ERR_INVALID_ARG
+    assert lib.deltanet_scan_bwd(*args(g, out, None, None, x, None, *more, None)) == L.DN_ERR_INVALID_ARG
+    assert lib.deltanet_scan_step(*args(x, g, state, None, out)) == L.DN_ERR_INVALID_ARG

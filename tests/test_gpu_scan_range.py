@@ -108,3 +108,31 @@ def test_a_subnormal_state_that_grows_past_one(x, g, split):
     want, bound = ops.scan_bwd(f64(gs.flip(1)), f64(xs), f64(dh), f64(s0), None, f64(df))
     few = ops.scan_bwd(f64(gs.flip(1)), f64(xs), sub)[0][0]
     close(dx[:, T - run:], want[0][:, T - run:], k * bound[0][:, T - run:] + few[:, T - run:], 2.0 ** -134)
+
+
+@pytest.mark.slow
+def test_the_widest_rows():
+    """The largest D that is taken, for the step and (fewer tokens than that fill the GPU) the
+    walkers; the last channels against the same channels alone."""
+    D = 2 ** 31 - 16385
+    gen = torch.Generator("cuda").manual_seed(0)
+    x = torch.zeros((1, 1, D), dtype=BF, device=DEV)
+    g = torch.full((1, 1, 1), -0.5, dtype=BF, device=DEV).expand(1, 1, D).contiguous()
+    state = torch.ones((1, D), device=DEV)
+    tail = slice(D - 5000, D)
+    for t in (x, state):
+        t[..., tail].copy_(torch.randn((5000,), generator=gen, device=DEV))
+    ref = state[:, tail].clone()
+    want = dn.deltanet_scan_step(x[..., tail], g[..., tail], ref)
+    got = dn.deltanet_scan_step(x, g, state)
+    assert torch.equal(got[..., tail], want) and torch.equal(state[:, tail], ref)
+    assert (state[:, :5] == state[0, 0]).all() and torch.equal(state[0, D // 2:D // 2 + 5], state[0, :5])
+    del got
+    out, fin = dn.deltanet_scan_fwd(x, g, state)
+    want, wfin = dn.deltanet_scan_fwd(x[..., tail], g[..., tail], state[:, tail])
+    assert torch.equal(out[..., tail], want) and torch.equal(fin[:, tail], wfin)
+    assert (out[0, 0, :5] == out[0, 0, D // 2]).all()
+    dx, dg, ds = dn.deltanet_scan_bwd(g, out, x, state)
+    want = dn.deltanet_scan_bwd(g[..., tail], out[..., tail], x[..., tail], state[:, tail])
+    for a, b in zip((dx, dg, ds), want):
+        assert torch.equal(a[..., tail], b)
