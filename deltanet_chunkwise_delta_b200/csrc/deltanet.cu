@@ -79,16 +79,26 @@ dn_status set_smem(K* kernel, int dev, int bytes) {
     return DN_OK;
 }
 
+// An error word at 0, ordered before what the stream does next (the legacy default stream,
+// which cudaMemset takes, is not ordered with a non-blocking one).
+dn_status new_flag(cudaStream_t stream, int** flag) {
+    int* f = nullptr;
+    if (cudaMalloc(&f, 256) != cudaSuccess) return DN_ERR_WORKSPACE;
+    if (cudaMemsetAsync(f, 0, 256, stream) != cudaSuccess) {
+        cudaFree(f);
+        return DN_ERR_CUDA;
+    }
+    *flag = f;
+    return DN_OK;
+}
+
 // Workspace of `bytes` for (dev, stream); grows stream-ordered.
 dn_status get_ws(int dev, cudaStream_t stream, size_t bytes, StreamWs& out) {
     std::lock_guard<std::mutex> lk(g_mu);
     StreamWs& w = g_ws[std::make_pair(dev, stream)];
     if (!w.flag) {
-        if (cudaMalloc(&w.flag, 256) != cudaSuccess) {
-            w.flag = nullptr;
-            return DN_ERR_WORKSPACE;
-        }
-        if (cudaMemset(w.flag, 0, 256) != cudaSuccess) return DN_ERR_CUDA;
+        const dn_status st = new_flag(stream, &w.flag);
+        if (st != DN_OK) return st;
     }
     if (bytes > w.cap) {
         if (w.buf) cudaFreeAsync(w.buf, stream);
@@ -715,8 +725,13 @@ dn_status deltanet_get_error(void* stream_ptr) {
     }
     if (flag) {
         int f = 0;
-        if (cudaMemcpy(&f, flag, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess) return DN_ERR_CUDA;
-        if (f != 0 && cudaMemset(flag, 0, sizeof f) != cudaSuccess) return DN_ERR_CUDA;
+        if (cudaMemcpyAsync(&f, flag, sizeof f, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+            cudaStreamSynchronize(stream) != cudaSuccess)
+            return DN_ERR_CUDA;
+        // clear before the caller goes on: a graph captured on this stream may be replayed on another
+        if (f != 0 && (cudaMemsetAsync(flag, 0, sizeof f, stream) != cudaSuccess ||
+                       cudaStreamSynchronize(stream) != cudaSuccess))
+            return DN_ERR_CUDA;
         if (h == 0) h = f;
     }
     if (h == kErrSeqlens) return DN_ERR_SEQLENS;

@@ -1,0 +1,72 @@
+"""The error word of a stream, which deltanet_get_error reads: reports reach the caller whatever
+other streams do meanwhile."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+
+import deltanet_chunkwise_delta_b200 as dn
+from deltanet_chunkwise_delta_b200 import _lib as L
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    dn.load()
+
+
+@contextlib.contextmanager
+def new_stream():
+    """A non-blocking stream that never had a call (torch's own come from a pool)."""
+    torch.cuda.current_stream()                        # there is a context
+    driver, handle = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+    assert driver.cuStreamCreate(ctypes.byref(handle), 1) == 0
+    s = torch.cuda.ExternalStream(handle.value)
+    yield s
+    s.synchronize()                                    # kept: its handle must not come again
+
+
+def rnd(*shape, dtype=BF, seed=0):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(DEV, dtype)
+
+
+def bad_slot():
+    x, g, cache = rnd(2, 1, 64), -rnd(2, 1, 64, dtype=F).abs(), rnd(2, 64, dtype=F)
+    slots, out = torch.tensor([1, 7], dtype=torch.int32, device=DEV), torch.empty_like(x)
+    return lambda: dn.deltanet_scan_step(x, g, cache, slots, out=out)
+
+
+def bad_boundary():
+    x, g, cu = rnd(1, 40, 64), -rnd(1, 40, 64, dtype=F).abs(), torch.tensor([0, 30, 39], dtype=torch.int32, device=DEV)
+    out, fin = torch.empty_like(x), torch.empty((2, 64), device=DEV)
+    return lambda: dn.deltanet_scan_fwd(x, g, None, cu, out, fin)
+
+
+def busy_default_stream():
+    """About 0.3 s of work on the default stream, behind which a memset there would wait."""
+    torch.cuda._sleep(600_000_000)
+
+
+@pytest.mark.parametrize("kind,error", [(bad_slot, L.DN_ERR_SLOTS), (bad_boundary, L.DN_ERR_SEQLENS)])
+def test_reports_while_the_default_stream_is_busy(kind, error):
+    """The stream's first call, which makes its word, and a call after a report was read."""
+    call = kind()
+    call()                                             # the kernel is loaded, which waits for the GPU
+    assert dn.get_error() == error
+    with new_stream() as s:
+        for _ in range(2):
+            torch.cuda.synchronize()
+            busy_default_stream()
+            with torch.cuda.stream(s):
+                call()
+                assert dn.get_error(s) == error        # read and cleared ..
+                call()
+                torch.cuda.synchronize()               # .. once, whatever else was under way
+                assert dn.get_error(s) == error
+                assert dn.get_error(s) == 0
