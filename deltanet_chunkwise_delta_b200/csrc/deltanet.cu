@@ -83,8 +83,12 @@ dn_status set_smem(K* kernel, int dev, int bytes) {
 // which cudaMemset takes, is not ordered with a non-blocking one).
 dn_status new_flag(cudaStream_t stream, int** flag) {
     int* f = nullptr;
-    if (cudaMalloc(&f, 256) != cudaSuccess) return DN_ERR_WORKSPACE;
+    if (cudaMalloc(&f, 256) != cudaSuccess) {
+        cudaGetLastError();                      // not the next call's
+        return DN_ERR_WORKSPACE;
+    }
     if (cudaMemsetAsync(f, 0, 256, stream) != cudaSuccess) {
+        cudaGetLastError();
         cudaFree(f);
         return DN_ERR_CUDA;
     }
@@ -92,10 +96,20 @@ dn_status new_flag(cudaStream_t stream, int** flag) {
     return DN_OK;
 }
 
-// Workspace of `bytes` for (dev, stream); grows stream-ordered.
+// Workspace of `bytes` for (dev, stream); grows stream-ordered.  Inside a capture it cannot:
+// memory of a graph's own would stay in the cache here for calls outside it (DN_ERR_WORKSPACE,
+// the capture goes on).
 dn_status get_ws(int dev, cudaStream_t stream, size_t bytes, StreamWs& out) {
     std::lock_guard<std::mutex> lk(g_mu);
     StreamWs& w = g_ws[std::make_pair(dev, stream)];
+    if (!w.flag || bytes > w.cap) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+            cudaGetLastError();
+            return DN_ERR_CUDA;
+        }
+        if (cap != cudaStreamCaptureStatusNone) return DN_ERR_WORKSPACE;
+    }
     if (!w.flag) {
         const dn_status st = new_flag(stream, &w.flag);
         if (st != DN_OK) return st;
@@ -767,9 +781,6 @@ dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create) 
         *flag = nullptr;
         return DN_OK;
     }
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return DN_ERR_CUDA;
-    if (cap != cudaStreamCaptureStatusNone) return DN_ERR_WORKSPACE;
     StreamWs ws;
     const dn_status st = get_ws(dev, stream, 0, ws);
     if (st == DN_OK) *flag = ws.flag;

@@ -83,6 +83,10 @@ typedef struct {
  * (invalid cu_seqlens contents, a bounded wait that ran out) are recorded in a
  * per-stream flag read by deltanet_get_error; in that case out/final_state are
  * unspecified.  Reentrant: calls on different streams use separate workspaces.
+ * A stream's workspace grows to its largest call: make a call of the size on the
+ * stream before capturing one (a capture in which it would have to grow gets
+ * DN_ERR_WORKSPACE and goes on without the call), and keep its later calls within
+ * that size while the graph lives, which uses the workspace that there was.
  */
 dn_status deltanet_fwd(const dn_tensor* q, const dn_tensor* k, const dn_tensor* v,
                        const dn_tensor* beta, const dn_tensor* initial_state,

@@ -1,5 +1,5 @@
-"""The error word of a stream, which deltanet_get_error reads: reports reach the caller whatever
-other streams do meanwhile."""
+"""The error word of a stream, which deltanet_get_error reads, and the workspace beside it: reports
+reach the caller whatever other streams do meanwhile, and captured calls leave both sound."""
 import contextlib
 import ctypes
 
@@ -70,3 +70,41 @@ def test_reports_while_the_default_stream_is_busy(kind, error):
                 torch.cuda.synchronize()               # .. once, whatever else was under way
                 assert dn.get_error(s) == error
                 assert dn.get_error(s) == 0
+
+
+def test_a_workspace_does_not_grow_inside_a_capture():
+    """A stream that had a token step (its error word exists, a workspace does not): the chunkwise
+    call captured on it is refused and the capture goes on; after a call of its size it is taken,
+    and eager calls, replays and larger calls follow in any order."""
+    q, k, v = (rnd(1, 200, 2, 128, seed=s) * 0.1 for s in (1, 2, 3))
+    beta = rnd(1, 200, 2, dtype=F, seed=4).sigmoid()
+    want, wfin = dn.deltanet_fwd(q, k, v, beta)
+    torch.cuda.synchronize()
+    with new_stream() as s:
+        with torch.cuda.stream(s):
+            bad_slot()()
+            assert dn.get_error(s) == L.DN_ERR_SLOTS
+        t = torch.zeros(1, device=DEV)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            with pytest.raises(dn.DeltaNetError) as e:
+                dn.deltanet_fwd(q, k, v, beta)
+            t += 1
+        assert e.value.status == L.DN_ERR_WORKSPACE
+        graph.replay()
+        torch.cuda.synchronize()
+        assert t.item() == 1
+        with torch.cuda.stream(s):
+            out, fin = dn.deltanet_fwd(q, k, v, beta)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(fin, wfin)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out, fin = dn.deltanet_fwd(q, k, v, beta)
+        for _ in range(2):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(fin, wfin)
+        assert dn.get_error(s) == 0
