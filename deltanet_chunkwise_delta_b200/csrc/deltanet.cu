@@ -799,9 +799,9 @@ void deltanet_release_workspace(void) {
         cudaSetDevice(kv.first.first);
         cudaDeviceSynchronize();
         if (kv.second.buf) cudaFree(kv.second.buf);
-        if (kv.second.flag) cudaFree(kv.second.flag);
+        kv.second.buf = nullptr;
+        kv.second.cap = 0;
     }
-    g_ws.clear();
     cudaSetDevice(cur);
 }
 

@@ -500,7 +500,9 @@ dn_status deltanet_get_error(void* stream);
  */
 void deltanet_test_set_wait(unsigned long long wait_ns, int stall_chunk);
 
-/* Frees every cached workspace (synchronises the device first). */
+/* Frees every cached workspace (synchronises the device first).  The streams' error
+ * words stay: graphs of calls that need no other workspace (deltanet_step,
+ * deltanet_scan_*) may be replayed after it, those of the forward passes may not. */
 void deltanet_release_workspace(void);
 
 /*

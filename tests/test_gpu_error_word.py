@@ -108,3 +108,21 @@ def test_a_workspace_does_not_grow_inside_a_capture():
             torch.cuda.synchronize()
             assert torch.equal(out, want) and torch.equal(fin, wfin)
         assert dn.get_error(s) == 0
+
+
+def test_captured_steps_outlive_the_workspaces():
+    """deltanet_release_workspace leaves what a captured step reports to."""
+    with new_stream() as s:
+        call = bad_slot()
+        with torch.cuda.stream(s):
+            call()
+            assert dn.get_error(s) == L.DN_ERR_SLOTS
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+        dn.release_workspace()
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(s):
+            graph.replay()
+            assert dn.get_error(s) == L.DN_ERR_SLOTS
+            assert dn.get_error(s) == 0
