@@ -80,20 +80,38 @@ dn_status set_smem(K* kernel, int dev, int bytes) {
 }
 
 // An error word at 0, ordered before what the stream does next (the legacy default stream,
-// which cudaMemset takes, is not ordered with a non-blocking one).
+// which cudaMemset takes, is not ordered with a non-blocking one).  It is made beside a capture,
+// not in it: allocated in relaxed mode and zeroed by a stream of its own that the host waits for,
+// since a zeroing in the graph would wipe what an earlier replay reported.
 dn_status new_flag(cudaStream_t stream, int** flag) {
-    int* f = nullptr;
-    if (cudaMalloc(&f, 256) != cudaSuccess) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
         cudaGetLastError();                      // not the next call's
-        return DN_ERR_WORKSPACE;
-    }
-    if (cudaMemsetAsync(f, 0, 256, stream) != cudaSuccess) {
-        cudaGetLastError();
-        cudaFree(f);
         return DN_ERR_CUDA;
     }
-    *flag = f;
-    return DN_OK;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return DN_ERR_CUDA;
+    dn_status st = DN_OK;
+    int* f = nullptr;
+    if (cudaMalloc(&f, 256) != cudaSuccess) {
+        st = DN_ERR_WORKSPACE;
+    } else if (cap == cudaStreamCaptureStatusNone) {
+        if (cudaMemsetAsync(f, 0, 256, stream) != cudaSuccess) st = DN_ERR_CUDA;
+    } else {
+        cudaStream_t own = nullptr;
+        if (cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) != cudaSuccess ||
+            cudaMemsetAsync(f, 0, 256, own) != cudaSuccess || cudaStreamSynchronize(own) != cudaSuccess)
+            st = DN_ERR_CUDA;
+        if (own) cudaStreamDestroy(own);
+    }
+    if (st != DN_OK) {
+        cudaGetLastError();
+        if (f) cudaFree(f);
+    } else {
+        *flag = f;
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return st;
 }
 
 // Workspace of `bytes` for (dev, stream); grows stream-ordered.  Inside a capture it cannot:
@@ -102,7 +120,7 @@ dn_status new_flag(cudaStream_t stream, int** flag) {
 dn_status get_ws(int dev, cudaStream_t stream, size_t bytes, StreamWs& out) {
     std::lock_guard<std::mutex> lk(g_mu);
     StreamWs& w = g_ws[std::make_pair(dev, stream)];
-    if (!w.flag || bytes > w.cap) {
+    if (bytes > w.cap) {
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
             cudaGetLastError();
@@ -769,21 +787,10 @@ void dn_wait_settings(unsigned long long* wait_ns, int* stall_chunk) {
 dn_status dn_device_check(int& dev, int& sms) { return device_check(dev, sms); }
 
 dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create) {
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        auto it = g_ws.find(std::make_pair(dev, stream));
-        if (it != g_ws.end() && it->second.flag) {
-            *flag = it->second.flag;
-            return DN_OK;
-        }
-    }
-    if (!create) {
-        *flag = nullptr;
-        return DN_OK;
-    }
-    StreamWs ws;
-    const dn_status st = get_ws(dev, stream, 0, ws);
-    if (st == DN_OK) *flag = ws.flag;
+    std::lock_guard<std::mutex> lk(g_mu);
+    StreamWs& w = g_ws[std::make_pair(dev, stream)];
+    const dn_status st = w.flag || !create ? DN_OK : new_flag(stream, &w.flag);
+    *flag = w.flag;
     return st;
 }
 

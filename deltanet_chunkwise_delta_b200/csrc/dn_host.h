@@ -16,8 +16,7 @@
 // The current device: its number and SM count; DN_ERR_UNSUPPORTED unless it is sm_100.
 DN_HIDDEN dn_status dn_device_check(int& dev, int& sms);
 // The error word of (dev, stream) that deltanet_get_error reads.  With `create` it is made on
-// first use, which allocates: inside a stream capture that is refused (DN_ERR_WORKSPACE), the
-// capture goes on.  Without, null where there is none yet.
+// first use, inside a stream capture too.  Without, null where there is none yet.
 DN_HIDDEN dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create = true);
 // What deltanet_last_launches reports for this thread's last successful call.
 DN_HIDDEN void dn_note_launches(int n);

@@ -331,9 +331,9 @@ dn_status deltanet_fwd_noalloc(const dn_tensor* q, const dn_tensor* k, const dn_
  * Layout rules as deltanet_fwd; state rows may not overlap each other.  state and
  * out may not overlap each other or any input (DN_ERR_ALIAS).  With
  * slot_idx the call uses its stream's error word, which the first such call on a
- * stream allocates: make that call before a capture (inside one it returns
- * DN_ERR_WORKSPACE, and the capture goes on).  Calls that overlap on the GPU may
- * not name the same rows.
+ * stream allocates (256 bytes; inside a capture too).  A replayed graph reports to
+ * the stream it was captured on: hand that one to deltanet_get_error.  Calls that
+ * overlap on the GPU may not name the same rows.
  */
 dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor* v,
                         const dn_tensor* beta, const dn_tensor* g, int n_h, dn_tensor* state,

@@ -126,3 +126,46 @@ def test_captured_steps_outlive_the_workspaces():
             graph.replay()
             assert dn.get_error(s) == L.DN_ERR_SLOTS
             assert dn.get_error(s) == 0
+
+
+@pytest.mark.parametrize("kind,error", [(bad_slot, L.DN_ERR_SLOTS), (bad_boundary, L.DN_ERR_SEQLENS)])
+def test_the_first_call_on_a_stream_may_be_captured(kind, error):
+    """As decoding is captured: nothing ran on the capture's stream before.  Every replay reports,
+    on any stream, and a report stays until it is read."""
+    call = kind()
+    call()
+    assert dn.get_error() == error
+    with new_stream() as s:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+        assert dn.get_error(s) == 0                    # captured, not run
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert dn.get_error(s) == error
+            assert dn.get_error(s) == 0
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dn.get_error(s) == error and dn.get_error() == 0
+
+
+def test_steps_captured_on_torchs_own_stream():
+    """torch.cuda.graph() without a stream, the usual way, and two graphs from it."""
+    x, g = rnd(3, 1, 64), -rnd(3, 1, 64, dtype=F).abs()
+    slots = torch.tensor([2, 0, 4], dtype=torch.int32, device=DEV)
+    caches = [rnd(5, 64, dtype=F, seed=s) for s in (1, 2)]
+    want = [c.clone() for c in caches]
+    outs = [[dn.deltanet_scan_step(x, g, c, slots) for _ in range(3)] for c in want]
+    graphs, got = [], []
+    for c in caches:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(dn.deltanet_scan_step(x, g, c, slots))
+    for t in range(3):
+        for i in (0, 1):
+            graphs[i].replay()
+            assert torch.equal(got[i], outs[i][t])
+    assert all(torch.equal(a, b) for a, b in zip(caches, want)) and dn.get_error() == 0
