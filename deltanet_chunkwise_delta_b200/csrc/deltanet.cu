@@ -786,10 +786,10 @@ void dn_wait_settings(unsigned long long* wait_ns, int* stall_chunk) {
 
 dn_status dn_device_check(int& dev, int& sms) { return device_check(dev, sms); }
 
-dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create) {
+dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag) {
     std::lock_guard<std::mutex> lk(g_mu);
     StreamWs& w = g_ws[std::make_pair(dev, stream)];
-    const dn_status st = w.flag || !create ? DN_OK : new_flag(stream, &w.flag);
+    const dn_status st = w.flag ? DN_OK : new_flag(stream, &w.flag);
     *flag = w.flag;
     return st;
 }

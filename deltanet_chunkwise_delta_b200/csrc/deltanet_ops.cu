@@ -92,10 +92,11 @@ dn_status scan_common(ScanParams& p, const dn_tensor* x, const dn_tensor* g, con
     p.x = x->data; p.x_sb = x->stride[0]; p.x_st = x->stride[1];
     p.g = g->data; p.g_sb = g->stride[0]; p.g_st = g->stride[1];
     p.B = (int)x->shape[0]; p.T = (int)x->shape[1]; p.D = (int)x->shape[2]; p.N = (int)N;
-    // packed input reports its boundaries through the error word; dense input would report a
-    // wait inside a cluster that gave up (its outputs are NaN then), where there is a word
-    if (cu) p.cu = static_cast<const int*>(cu->data);
-    return dn_stream_flag(dev, stream, &p.err, cu != nullptr);
+    dn_wait_settings(&p.wait_ns, &p.stall);
+    if (!p.wait_ns) p.wait_ns = sm100::kDefaultWaitNs;
+    if (!cu) return DN_OK;
+    p.cu = static_cast<const int*>(cu->data);
+    return dn_stream_flag(dev, stream, &p.err);
 }
 
 // Pairs of channels can move as one access: even D, strides and addresses.
@@ -157,7 +158,7 @@ int scan_wide(const ScanParams& p, int32_t x, int32_t g) {
 }
 
 template <typename X, typename G, bool PACKED, bool BWD, bool EVEN>
-dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
+dn_status scan_tiled(ScanParams& p, int dev, int sms, cudaStream_t stream) {
     const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 63) / 64);
     // Held runs where the instructions bound the tiles, and tokens per run as many as registers
     // or two CTAs' shared memory allow.  Held and read twice: rows of one CTA, 8 x 2048 x 2048,
@@ -176,6 +177,9 @@ dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
     if (items > kMax31 / K) return DN_ERR_INVALID_ARG;
     auto go = [&](auto* kern, int threads, int smem, int most) { return scan_launch(kern, items, K, threads, smem, most, stream, p, wide); };
     if (K > 1) {
+        // a wait inside a cluster that gives up is reported (packed input has its word)
+        const dn_status st = p.err ? DN_OK : dn_stream_flag(dev, stream, &p.err);
+        if (st != DN_OK) return st;
         constexpr int th = kScanThreadsOf<HK>;
         const int smem = part + K * 1024, most = part + kScanMaxCluster * 1024;
         if constexpr (BWD) return go(k_scan_bwd_piped<X, G, TK, PACKED, true, EVEN, HK>, th, smem, most);
@@ -187,7 +191,7 @@ dn_status scan_tiled(const ScanParams& p, int sms, cudaStream_t stream) {
 }
 
 template <bool BWD>
-dn_status scan_run(const ScanParams& p, int32_t x, int32_t g, cudaStream_t stream) {
+dn_status scan_run(ScanParams& p, int32_t x, int32_t g, cudaStream_t stream) {
     int dev = 0, sms = 0;
     dn_status st = dn_device_check(dev, sms);
     if (st != DN_OK) return st;
@@ -207,9 +211,9 @@ dn_status scan_run(const ScanParams& p, int32_t x, int32_t g, cudaStream_t strea
                 else k_scan_serial<X, G, 1><<<grid, kScanWalkers, 0, stream>>>(p);
             }
         } else if (even) {
-            st = p.cu ? scan_tiled<X, G, true, BWD, true>(p, sms, stream) : scan_tiled<X, G, false, BWD, true>(p, sms, stream);
+            st = p.cu ? scan_tiled<X, G, true, BWD, true>(p, dev, sms, stream) : scan_tiled<X, G, false, BWD, true>(p, dev, sms, stream);
         } else {
-            st = p.cu ? scan_tiled<X, G, true, BWD, false>(p, sms, stream) : scan_tiled<X, G, false, BWD, false>(p, sms, stream);
+            st = p.cu ? scan_tiled<X, G, true, BWD, false>(p, dev, sms, stream) : scan_tiled<X, G, false, BWD, false>(p, dev, sms, stream);
         }
     });
     return st == DN_OK ? launched(1) : st;

@@ -15,9 +15,11 @@
 // Defined in deltanet.cu.
 // The current device: its number and SM count; DN_ERR_UNSUPPORTED unless it is sm_100.
 DN_HIDDEN dn_status dn_device_check(int& dev, int& sms);
-// The error word of (dev, stream) that deltanet_get_error reads.  With `create` it is made on
-// first use, inside a stream capture too.  Without, null where there is none yet.
-DN_HIDDEN dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag, bool create = true);
+// The error word of (dev, stream) that deltanet_get_error reads, made on first use, inside a
+// stream capture too.
+DN_HIDDEN dn_status dn_stream_flag(int dev, cudaStream_t stream, int** flag);
+// This thread's deltanet_test_set_wait.
+DN_HIDDEN void dn_wait_settings(unsigned long long* wait_ns, int* stall_chunk);
 // What deltanet_last_launches reports for this thread's last successful call.
 DN_HIDDEN void dn_note_launches(int n);
 

@@ -24,6 +24,8 @@ struct ScanParams {
     int64_t x_sb, x_st, g_sb, g_st, h_sb, h_st, y_sb, y_st, dg_sb, dg_st;
     int64_t s0_sn, sT_sn, fin_sn;
     int B, T, D, N;
+    int stall;                   // > 0 (a test): a cluster's first CTA sends nothing at tile stall - 1
+    unsigned long long wait_ns;  // a wait inside a cluster gives up after so long
 };
 
 // Packed input: every CTA clamps its token range, the first reports boundaries that are not
@@ -390,8 +392,8 @@ constexpr int kBarRuns = 1, kBarCin = 2;   // named barriers: runs of a tile for
 
 // Waits for a phase that other CTAs of the cluster complete and acquires what they sent (a
 // fence in its place would also wait for this warp's own sends to land: 0.6 us a tile).  Gives
-// up after 2 s.
-__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity) {
+// up after limit_ns.
+__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (int i = 0;; ++i) {
         uint32_t ok;
@@ -403,17 +405,22 @@ __device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity
             : "memory");
         if (ok) return true;
         if (i == 255) t0 = sm100::globaltimer();
-        if (i > 255 && sm100::globaltimer() - t0 > sm100::kDefaultWaitNs) return false;
+        if (i > 255 && sm100::globaltimer() - t0 > limit_ns) return false;
     }
 }
 
 // The last warp: tile after tile, the runs of this CTA joined and exchanged.  carry: what comes
 // into the first tile, in the end what leaves the last one.
+//
+// A wait that gives up ends the CTA's part in the exchange: it arrives on no barrier whose phase
+// may be open and sends nothing more, so that the others give up in turn, a tile later at most.
+// Its warps get NaN for what comes into their runs from that tile on; sequences that start in
+// them are right.  Returns the tile, or -1.
 template <bool PACKED, bool CL, int W>
-__device__ __forceinline__ void scan_join(ScanRuns<W, CL>& sm, float4* cta, int tiles, int K,
-                                          unsigned rank, float* carry, int* err) {
+__device__ __forceinline__ int scan_join(ScanRuns<W, CL>& sm, float4* cta, int tiles, int K, unsigned rank,
+                                         float* carry, const ScanParams& p) {
     const int lane = threadIdx.x & 31;
-    bool ok = true;
+    int gave = -1;
     for (int i = 0; i < tiles; ++i) {
         const int par = i & 1;
         bar_sync(kBarRuns, (W + 1) * 32);
@@ -432,7 +439,7 @@ __device__ __forceinline__ void scan_join(ScanRuns<W, CL>& sm, float4* cta, int 
             };
             if (far) through(std::true_type());
             else through(std::false_type());
-        } else {
+        } else if (gave < 0) {
             // the runs ahead of each warp's as one map.  The product of their factors where that is
             // one factor as well; else from the sum of their logarithms, which the chain over the
             // warps would wait for (in every tile: 65536 x 512 a tenth longer).
@@ -459,7 +466,8 @@ __device__ __forceinline__ void scan_join(ScanRuns<W, CL>& sm, float4* cta, int 
             }
             if (lane == 0) sm100::mbar_expect_tx(&sm.full[par], K * 512);
             const uint32_t dst = sm100::saddr(cta + (par * K + rank) * 32 + lane), bar = sm100::saddr(&sm.full[par]);
-            for (int r = 0; r < K; ++r) {
+            const int to = rank == 0 && p.stall == i + 1 ? 0 : K;
+            for (int r = 0; r < to; ++r) {
                 uint32_t d, m;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dst), "r"(r));
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(bar), "r"(r));
@@ -469,39 +477,48 @@ __device__ __forceinline__ void scan_join(ScanRuns<W, CL>& sm, float4* cta, int 
                     "r"(__float_as_uint(all.w)), "r"(m)
                     : "memory");
             }
-            ok = ok && cluster_mbar_wait(&sm.full[par], i >> 1 & 1);
-            // without the others' runs nothing after them is known: NaN, not numbers of some kind
-            if (!ok) carry[0] = carry[1] = __uint_as_float(0x7fffffffu);
-            float c0 = 0.f, c1 = 0.f;
-            const float before[2] = {carry[0], carry[1]};
-            bool again = false;
-            for (int r = 0; r < K; ++r) {
-                if (r == (int)rank) c0 = carry[0], c1 = carry[1];
-                const float4 run = cta[(par * K + r) * 32 + lane];
-                again |= run.x < 0.f || run.y < 0.f;
-                run_through<PACKED, false>(run, carry[0], carry[1]);
-            }
-            if (again) {
-                carry[0] = before[0], carry[1] = before[1];
+            if (!__all_sync(~0u, cluster_mbar_wait(&sm.full[par], i >> 1 & 1, p.wait_ns))) {
+                gave = i;
+                // what the others may have sent for the next tile (for no later one) lands on its barrier
+                if (lane == 0 && i + 1 < tiles) sm100::mbar_expect_tx(&sm.full[par ^ 1], K * 512);
+            } else {
+                float c0 = 0.f, c1 = 0.f;
+                const float before[2] = {carry[0], carry[1]};
+                bool again = false;
                 for (int r = 0; r < K; ++r) {
                     if (r == (int)rank) c0 = carry[0], c1 = carry[1];
-                    run_through<PACKED, true>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
+                    const float4 run = cta[(par * K + r) * 32 + lane];
+                    again |= run.x < 0.f || run.y < 0.f;
+                    run_through<PACKED, false>(run, carry[0], carry[1]);
                 }
-            }
-            auto into = [&](auto any) {
+                if (again) {
+                    carry[0] = before[0], carry[1] = before[1];
+                    for (int r = 0; r < K; ++r) {
+                        if (r == (int)rank) c0 = carry[0], c1 = carry[1];
+                        run_through<PACKED, true>(cta[(par * K + r) * 32 + lane], carry[0], carry[1]);
+                    }
+                }
+                auto into = [&](auto any) {
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    float x0 = c0, x1 = c1;
-                    run_through<PACKED, decltype(any)::value>(pre[w], x0, x1);
-                    *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
-                }
-            };
-            if (far) into(std::true_type());
-            else into(std::false_type());
+                    for (int w = 0; w < W; ++w) {
+                        float x0 = c0, x1 = c1;
+                        run_through<PACKED, decltype(any)::value>(pre[w], x0, x1);
+                        *reinterpret_cast<float2*>(&sm.warp[w][lane]) = make_float2(x0, x1);
+                    }
+                };
+                if (far) into(std::true_type());
+                else into(std::false_type());
+            }
         }
+        if (CL && gave >= 0)
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                *reinterpret_cast<float2*>(&sm.warp[w][lane]) =
+                    make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
         bar_arrive(kBarCin, (W + 1) * 32);
     }
-    if (!ok && lane == 0 && err) *err = kErrTimeout;
+    if (gave >= 0 && lane == 0) *p.err = kErrTimeout;
+    return gave;
 }
 
 // Before and after the work of a CTA of a cluster: barriers of the exchange ready everywhere,
@@ -526,6 +543,14 @@ __device__ __forceinline__ void scan_leave() {
         cluster_arrive();
         cluster_wait();
     }
+}
+// The joining warp's: where it gave up, the others' sends of that tile and the next, all of them
+// under way by now, are waited for (200 ms each where one was never sent).
+template <bool CL, int W>
+__device__ __forceinline__ void scan_leave(ScanRuns<W, CL>& sm, int gave, int tiles) {
+    scan_leave<CL>();
+    if (CL && gave >= 0)
+        for (int i = gave; i < min(gave + 2, tiles); ++i) sm100::mbar_drain(&sm.full[i & 1], i >> 1 & 1);
 }
 
 // The last n with cu[n] <= t, looked for outwards from `near`; in 0 .. N - 1 whatever cu holds.
@@ -633,12 +658,12 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
         if (live1) carry[1] = p.s0[b * p.s0_sn + c + 1];
     }
     if (w == W) {
-        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p.err);
+        const int gave = scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
-        scan_leave<CL>();
+        scan_leave<CL, W>(sm, gave, tiles);
         return;
     }
     auto initial = [&](int n, float* s) {      // the start state of sequence n
@@ -815,12 +840,12 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
         if (live1) carry[1] = p.sT[b * p.sT_sn + c + 1];
     }
     if (w == W) {
-        scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p.err);
+        const int gave = scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p);
         if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
             p.fin[b * p.fin_sn + c] = carry[0];
             if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
         }
-        scan_leave<CL>();
+        scan_leave<CL, W>(sm, gave, tiles);
         return;
     }
     auto state = [&](const float* src, int64_t sn, int n, float* s) {

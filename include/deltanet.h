@@ -369,7 +369,9 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
  * cu_seqlens contents that deltanet_get_error reports as DN_ERR_SEQLENS the outputs
  * are unspecified.  The result does not depend on timing: the same call gives the
  * same bits.  (Long rows are split across a thread-block cluster; a wait in it that
- * gave up after 2 s would leave NaN behind it.)
+ * gives up, after 2 s, is reported as DN_ERR_TIMEOUT and leaves NaN behind it, up to
+ * where a sequence starts.  For that report a dense call with such rows uses its
+ * stream's error word too.)
  */
 dn_status deltanet_scan_fwd(const dn_tensor* x, const dn_tensor* g,
                             const dn_tensor* initial_state, const dn_tensor* cu_seqlens,
@@ -495,8 +497,10 @@ dn_status deltanet_get_error(void* stream);
  * stall_chunk - 1 of every run, on a barrier that nothing completes, so that
  * the wait runs out: the kernel then gives up, waits for its copies and
  * products in flight, frees its tensor memory, exits and reports the
- * time-out.  The outputs of such a call are unspecified.  0 (the default):
- * no stall.  deltanet_test_set_wait(0, 0) restores normal calls.
+ * time-out.  The outputs of such a call are unspecified.  In deltanet_scan_fwd
+ * and _bwd, where rows are split across a cluster: its first CTA sends the
+ * others nothing at tile stall_chunk - 1, and their waits (its own too) run out.
+ * 0 (the default): no stall.  deltanet_test_set_wait(0, 0) restores normal calls.
  */
 void deltanet_test_set_wait(unsigned long long wait_ns, int stall_chunk);
 
