@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -33,3 +34,11 @@ def pytest_terminal_summary(terminalreporter, exitstatus, config):
     for name, eo, es, bar in log:
         es_s = f"{es:.3e}" if es is not None else "-"
         terminalreporter.write_line(f"{name:<40s} out {eo:.3e}  final_state {es_s}  (bar {bar:g})")
+
+
+# test_gpu_calls counts allocated memory: tensors that earlier tests left in reference cycles
+# (an exception's frames) go before a test, not during it.
+@pytest.fixture(autouse=True)
+def _garbage(request):
+    if request.module.__name__.endswith("test_gpu_calls"):
+        gc.collect()
