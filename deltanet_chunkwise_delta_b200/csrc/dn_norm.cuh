@@ -72,15 +72,18 @@ __device__ __forceinline__ E* row_ptr(const RowRef& r, unsigned i0, unsigned i1,
     return static_cast<E*>(const_cast<void*>(r.p)) + i0 * r.s0 + i1 * r.s1 + i2 * r.s2;
 }
 
-// act(z) and act'(z) from s = 1 / (1 + e^-z): the hardware's 2^x and 1/x, a few ulp each.  Far
-// out e^-z is inf or 0 and s is 0 or 1.
+// act(z) and act'(z) from s = 1 / (1 + e^-z): the hardware's 2^x and 1/x, a few ulp each and
+// what |z| ulp the exponential adds.  Far out e^-z is inf or 0 and s is 0 or 1.  1 - s is e^-z s:
+// the difference has no figures left where s is near 1 (none at z = 17), and the sigmoid's
+// derivative s (1 - s) would have none.
 __device__ __forceinline__ float norm_act(float z, int act, float* grad = nullptr) {
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
+    const float e = __expf(-z), s = __fdividef(1.f, 1.f + e);
+    const float rest = __saturatef(e * s);             // 1 - s; at s = 0 0 as well, not inf times 0
     if (act == 1) {
-        if (grad) *grad = s * (1.f - s);
+        if (grad) *grad = s * rest;
         return s;
     }
-    if (grad) *grad = s * (1.f + z * (1.f - s));
+    if (grad) *grad = s * (1.f + z * rest);
     return z * s;
 }
 

@@ -78,8 +78,8 @@ def scan_bwd(g, h, dh, init=None, cu=None, dfinal=None):
 # ---- norms around a block ------------------------------------------------------
 
 def act(z, kind):
-    s = 1.0 / (1.0 + np.exp(-z))
-    return (z * s, s * (1.0 + z * (1.0 - s))) if kind == "silu" else (s, s * (1.0 - s))
+    s, one_less = 1.0 / (1.0 + np.exp(-z)), 1.0 / (1.0 + np.exp(z))       # and 1 - s
+    return (z * s, s * (1.0 + z * one_less)) if kind == "silu" else (s, s * one_less)
 
 
 def _chain(y, w, z, kind, r, s, eps):
@@ -150,8 +150,7 @@ def norm_bwd(y, dout, w=None, z=None, kind="silu", r=None, s=None, nw=None, drou
             dv, mv = dv * s, mv * np.abs(s)
     if z is not None:
         # act' of silu is a difference that cancels near z = -1.28: its magnitude
-        sg = 1.0 / (1.0 + np.exp(-z))
-        mda = sg * (1.0 + np.abs(z)) if kind == "silu" else sg
+        mda = (1.0 + np.abs(z)) / (1.0 + np.exp(-z)) if kind == "silu" else da
         out["gate"], bnd["gate"] = dv * y1 * da, K * mv * np.abs(y1) * mda
         dv, mv = dv * a, mv * np.abs(a)
     if w is not None:
