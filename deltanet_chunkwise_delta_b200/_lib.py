@@ -16,6 +16,7 @@ import importlib.util
 import os
 import struct
 import threading
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -430,18 +431,32 @@ def _descriptors(*tensors):
 _call = None
 
 
+class _General:
+    """In the place of csrc/dn_call.cpp where it is missing or made for another torch: every call
+    goes the general way, to the same kernels."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _short():
     """The calls that need no marshalling here (csrc/dn_call.cpp): each takes its binding's
     arguments and answers None where they want the general way below."""
     global _call
     if _call is None:
         load()
-        if not os.path.exists(_build.CALL):
-            raise RuntimeError(f"{_build.CALL} not found; run "
-                               "`python -m deltanet_chunkwise_delta_b200.build`")
-        loader = importlib.machinery.ExtensionFileLoader("dn_call", _build.CALL)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dn_call", loader))
-        loader.exec_module(module)
+        why = "missing or made for another torch"
+        module = _General()
+        if _build.call_usable():
+            try:
+                loader = importlib.machinery.ExtensionFileLoader("dn_call", _build.CALL)
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dn_call", loader))
+                loader.exec_module(module)
+            except ImportError as e:
+                why, module = str(e), _General()
+        if isinstance(module, _General):
+            warnings.warn(f"{_build.CALL}: {why}; calls take longer without it (run "
+                          "`python -m deltanet_chunkwise_delta_b200.build`)", RuntimeWarning, stacklevel=3)
         _call = module
     return _call
 

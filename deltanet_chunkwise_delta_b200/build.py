@@ -3,7 +3,8 @@
 ``python -m deltanet_chunkwise_delta_b200.build`` compiles the ``csrc/*.cu``
 files with nvcc into ``_build/libdeltanet_b200.so`` inside the package directory, so
 the library travels with the source tree, and ``csrc/dn_call.cpp``, the binding's short
-way to it, with g++ into ``_build/dn_call.so`` beside it.
+way to it, with g++ into ``_build/dn_call.so`` beside it.  That one is made for one torch and
+one Python (named in ``_build/dn_call.abi``); where it cannot be made, the binding does without.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ SRCS = [os.path.join(PKG, "csrc", name)
         for name in ("deltanet.cu", "deltanet_noalloc.cu", "deltanet_ops.cu", "deltanet_norm.cu")]
 LIB = os.path.join(PKG, "_build", "libdeltanet_b200.so")
 CALL = os.path.join(PKG, "_build", "dn_call.so")
+CALL_SRCS = [os.path.join(PKG, "csrc", "dn_call.cpp"), os.path.join(ROOT, "include", "deltanet.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -31,15 +33,33 @@ NVCC_FLAGS = [
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + \
+    return [s for s in sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) if s != CALL_SRCS[0]] + \
         [os.path.join(ROOT, "include", "deltanet.h")]
 
 
+def _older(path: str, sources) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
-    return any(os.path.getmtime(s) > t for s in _sources())
+    return _older(LIB, _sources())
+
+
+def abi() -> str:
+    """The torch and the Python that CALL has to be made for."""
+    import torch
+    return f"torch {torch.__version__} {sys.implementation.cache_tag}"
+
+
+def call_usable() -> bool:
+    """CALL is there and made for this torch and this Python."""
+    if not os.path.exists(CALL):
+        return False
+    try:
+        with open(CALL[:-3] + ".abi") as f:
+            return f.read() == abi()
+    except OSError:
+        return False
 
 
 def _run(cmd, verbose):
@@ -63,12 +83,25 @@ def _build_call(verbose: bool) -> None:
           "-l:" + os.path.basename(LIB), "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
           "-ltorch", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, CALL)
+    with open(CALL[:-3] + ".abi", "w") as f:
+        f.write(abi())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
+    if force or stale():
+        _build_lib(verbose)
+    if force or _older(CALL, CALL_SRCS) or not call_usable():
+        try:
+            _build_call(verbose)
+        except (OSError, RuntimeError) as e:    # no g++, no Python headers: the calls go through ctypes
+            if os.path.exists(CALL):
+                os.remove(CALL)
+            sys.stderr.write(f"{CALL} was not built, calls take longer without it: {e}\n")
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, *SRCS]
@@ -77,8 +110,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with open(log, "w") as f:
         f.write(err)
     os.replace(tmp, LIB)
-    _build_call(verbose)
-    return LIB
 
 
 if __name__ == "__main__":
