@@ -182,11 +182,11 @@ dn_status scan_tiled(ScanParams& p, int dev, int sms, cudaStream_t stream) {
         if (st != DN_OK) return st;
         constexpr int th = kScanThreadsOf<HK>;
         const int smem = part + K * 1024, most = part + kScanMaxCluster * 1024;
-        if constexpr (BWD) return go(k_scan_bwd_piped<X, G, TK, PACKED, true, EVEN, HK>, th, smem, most);
+        if constexpr (BWD) return go(k_scan_bwd_piped<X, G, TK, PACKED, true, EVEN>, th, smem, most);
         else return go(k_scan_piped<X, G, TK, PACKED, true, EVEN, HK>, th, smem, most);
     }
     constexpr int th = kScanThreadsOf<H1>;
-    if constexpr (BWD) return go(k_scan_bwd_piped<X, G, T1, PACKED, false, EVEN, H1>, th, stage, stage);
+    if constexpr (BWD) return go(k_scan_bwd_piped<X, G, T1, PACKED, false, EVEN>, th, stage, stage);
     else return go(k_scan_piped<X, G, T1, PACKED, false, EVEN, H1>, th, stage, stage);
 }
 

@@ -191,9 +191,9 @@ __global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) 
 // runs, sends the CTA's to the cluster's other CTAs (st.async on their mbarriers), waits for
 // theirs and hands every warp the h before its run, all of it behind the finishing of the tile
 // before.  A tile is finished by running its recurrence again from the h that comes in.  Its
-// tokens and decays stay in registers until then (HELD: seven warps and the joining one, 128
-// registers), or are read again (eight and one, 96 registers; the decays of an fp32 gate have
-// taken its place in shared memory, of a bf16 gate the power is taken twice): fewer
+// tokens and decays stay in registers until then (HELD, forward: seven warps and the joining
+// one, 128 registers), or are read again (eight and one, 96 registers; the decays of an fp32 gate
+// have taken its place in shared memory, of a bf16 gate the power is taken twice): fewer
 // instructions and longer runs against one warp more.
 //
 // B200: forward of 8 x 2048 x 2048 (bf16, fp32 gates) 51 us, 80 % of the measured copy rate
@@ -659,10 +659,6 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
     }
     if (w == W) {
         const int gave = scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p);
-        if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
-            p.fin[b * p.fin_sn + c] = carry[0];
-            if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
-        }
         scan_leave<CL, W>(sm, gave, tiles);
         return;
     }
@@ -760,10 +756,8 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
     };
     Held even, odd;
     int s = 0;
-    if (tiles > 0) {
-        cp_async_wait<kScanStages - 1>();
-        next(t0, 0, even);
-    }
+    cp_async_wait<kScanStages - 1>();
+    next(t0, 0, even);
     auto tile = [&](int i, Held& now, Held& then) {
         bar_sync(kBarCin, kScanThreadsOf<HELD>);
         const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
@@ -797,10 +791,10 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_piped(ScanPara
     scan_leave<CL>();
 }
 
-template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN, bool HELD>
-__global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
+template <typename X, typename G, int TS, bool PACKED, bool CL, bool EVEN>
+__global__ void __launch_bounds__(kScanThreadsOf<false>, 2) k_scan_bwd_piped(ScanParams p, int K, int wide) {
     extern __shared__ __align__(128) unsigned char dyn[];
-    constexpr int W = kScanWarps<HELD>;
+    constexpr int W = kScanWarps<false>;
     using Stage = ScanStage<X, G, TS, true, W>;       // then [2][K][32] float4: the CTAs' runs
     Stage& st = *reinterpret_cast<Stage*>(dyn + kScanPlace<true>);
     __shared__ ScanRuns<W, CL> sm;
@@ -841,10 +835,6 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
     }
     if (w == W) {
         const int gave = scan_join<PACKED, CL, W>(sm, reinterpret_cast<float4*>(&st + 1), tiles, K, rank, carry, p);
-        if (!PACKED && p.T == 0 && p.fin && live && rank == 0) {
-            p.fin[b * p.fin_sn + c] = carry[0];
-            if (live1) p.fin[b * p.fin_sn + c + 1] = carry[1];
-        }
         scan_leave<CL, W>(sm, gave, tiles);
         return;
     }
@@ -854,10 +844,6 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
     };
     using XR = typename RawVec<X, 2>::T;
     using GR = typename RawVec<G, 2>::T;
-    struct Held {                              // the tokens of a run
-        XR d[TS], h[TS];
-        float a[TS][2];
-    };
     auto read = [&](int s, XR* rd, GR* rg) {
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
@@ -869,34 +855,32 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
 #pragma unroll
         for (int j = 0; j < TS; ++j) rh[j] = ld_raw<X, 2>(&st.h[s][w][j][lane * 2]);
     };
-    auto form = [&](int s, unsigned ends, int own, Held& hd) {
+    auto form = [&](int s, unsigned ends, int own) {
         float e[2] = {0.f, 0.f}, L[2] = {0.f, 0.f};
+        XR rd[TS];
         GR rg[TS];
-        read(s, hd.d, rg);
-        if (HELD) read_h(s, hd.h);
+        read(s, rd, rg);
 #pragma unroll
         for (int j = 0; j < TS; ++j) {
             float dv[2], a[2];
-            unpack(hd.d[j], dv);
+            unpack(rd[j], dv);
             unpack(rg[j], a);
             scan_log2(a);
             add2(L, a, L);
             a[0] = scan_pow2(a[0]);
             a[1] = scan_pow2(a[1]);
-            if constexpr (HELD) hd.a[j][0] = a[0], hd.a[j][1] = a[1];
-            else if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
+            if constexpr (sizeof(G) == 4) st_vec<G, 2>(&st.g[s][w][j][lane * 2], a);
             if (PACKED && (ends >> j & 1)) state(p.sT, p.sT_sn, __shfl_sync(~0u, own, j), e);
             add2(dv, e, e);
             mul2(a, e, e);
         }
         sm.put(w, L, e, PACKED && ends);
     };
-    auto finish = [&](int t, int s, Held& hd, unsigned starts, unsigned ends, int own) {
+    auto finish = [&](int t, int s, unsigned starts, unsigned ends, int own) {
+        XR rd[TS], rh[TS];
         GR rg[TS];
-        if (!HELD) {
-            read(s, hd.d, rg);
-            read_h(s, hd.h);
-        }
+        read(s, rd, rg);
+        read_h(s, rh);
         // places up to `left` hold tokens; dense: place left - 1 of the last tile is token 0
         const int left = max(0, min(TS, t + 1));
         const bool at0 = !PACKED && left > 0 && t < TS;
@@ -905,18 +889,13 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
 #pragma unroll
         for (int j = 0; j < TS; ++j, ox -= p.y_st, og -= p.dg_st) {
             float dv[2], a[2], hv[2];
-            unpack(hd.d[j], dv);
-            unpack(hd.h[j], hv);
-            if constexpr (HELD) {
-                a[0] = hd.a[j][0];
-                a[1] = hd.a[j][1];
-            } else {
-                unpack(rg[j], a);
-                if constexpr (sizeof(G) == 2) {
-                    scan_log2(a);
-                    a[0] = scan_pow2(a[0]);
-                    a[1] = scan_pow2(a[1]);
-                }
+            unpack(rd[j], dv);
+            unpack(rh[j], hv);
+            unpack(rg[j], a);
+            if constexpr (sizeof(G) == 2) {
+                scan_log2(a);
+                a[0] = scan_pow2(a[0]);
+                a[1] = scan_pow2(a[1]);
             }
             int n = b;
             if (PACKED && ((starts | ends) >> j & 1)) n = __shfl_sync(~0u, own, j);
@@ -942,56 +921,39 @@ __global__ void __launch_bounds__(kScanThreadsOf<HELD>, 2) k_scan_bwd_piped(Scan
         }
     };
     ScanSeq<TS, -1> seq;
-    auto next = [&](int t, int s, Held& hd) {   // the run of a tile that has landed
+    auto next = [&](int t, int s) {            // the run of a tile that has landed
         __syncwarp();
         unsigned cut = 0;
         if (PACKED) {
             seq.find(p, t, p.sT, p.sT_sn, c);
             cut = seq.ends;
         }
-        if (PACKED && cut) form(s, cut, seq.own, hd);
-        else form(s, 0u, 0, hd);
-        bar_arrive(kBarRuns, kScanThreadsOf<HELD>);
-        if (HELD) {                              // its place is free
-            __syncwarp();
-            load(t - kScanStages * step, s);
-        }
+        if (PACKED && cut) form(s, cut, seq.own);
+        else form(s, 0u, 0);
+        bar_arrive(kBarRuns, kScanThreadsOf<false>);
     };
-    Held even, odd;
     int s = 0;
-    if (tiles > 0) {
-        cp_async_wait<kScanStages - 1>();
-        next(t0, 0, even);
-    }
-    auto tile = [&](int i, Held& now, Held& then) {
-        bar_sync(kBarCin, kScanThreadsOf<HELD>);
+    cp_async_wait<kScanStages - 1>();
+    next(t0, 0);
+    for (int i = 0; i < tiles; ++i) {
+        bar_sync(kBarCin, kScanThreadsOf<false>);
         const float2 in = *reinterpret_cast<const float2*>(&sm.warp[w][lane]);
         cin[0] = in.x;
         cin[1] = in.y;
         const unsigned starts = seq.starts, ends = seq.ends;
-        const int own = seq.own, s1 = s + 1 == kScanStages ? 0 : s + 1;
+        const int s1 = s + 1 == kScanStages ? 0 : s + 1;
         if (i + 1 < tiles) {
-            cp_async_wait<HELD ? kScanStages - 1 : kScanStages - 2>();
-            next(t0 - step, s1, then);
+            cp_async_wait<kScanStages - 2>();
+            next(t0 - step, s1);
         }
-        if (PACKED && (starts | ends)) finish(t0, s, now, starts, ends, HELD ? own : seq.owner(p, t0));   // (registers, or a search)
-        else finish(t0, s, now, 0u, 0u, 0);
-        if (!HELD) {
-            __syncwarp();
-            load(t0 - kScanStages * step, s);
-        }
+        if (PACKED && (starts | ends)) finish(t0, s, starts, ends, seq.owner(p, t0));    // (registers, or a search)
+        else finish(t0, s, 0u, 0u, 0);
+        __syncwarp();
+        load(t0 - kScanStages * step, s);
         s = s1;
         t0 -= step;
         dx -= dx_tile;
         dg -= dg_tile;
-    };
-    if constexpr (HELD) {
-        for (int i = 0; i < tiles; i += 2) {
-            tile(i, even, odd);
-            if (i + 1 < tiles) tile(i + 1, odd, even);
-        }
-    } else {
-        for (int i = 0; i < tiles; ++i) tile(i, even, odd);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     scan_leave<CL>();
