@@ -77,7 +77,7 @@ dn_status scan_shapes(const dn_tensor* x, const dn_tensor* g, const dn_tensor* c
     if (cu) {
         if (!index_ok(cu, 1) || B != 1) return DN_ERR_INVALID_ARG;
         N = cu->shape[0] - 1;
-        if (N >= (int64_t(1) << 24)) return DN_ERR_INVALID_ARG;
+        if (N >= (int64_t(1) << 24) || (N == 0 && T > 0)) return DN_ERR_INVALID_ARG;   // (tokens of no sequence)
     }
     if (N > 0 && (D + kScanWalkers - 1) / kScanWalkers > kMax31 / N) return DN_ERR_INVALID_ARG;   // a grid's CTAs
     return DN_OK;

@@ -356,7 +356,7 @@ dn_status deltanet_step(const dn_tensor* q, const dn_tensor* k, const dn_tensor*
  *   g             [B, T, D]   fp32, or bf16 with bf16 x: ln a.  Any value but NaN and
  *                             +inf makes sense; -inf is a = 0 (the channel forgets).
  *   initial_state [N, D] fp32, or NULL for zeros
- *   cu_seqlens    as deltanet_fwd (B must be 1), or NULL
+ *   cu_seqlens    as deltanet_fwd (B must be 1; N = 0 only with T = 0), or NULL
  *   out           [B, T, D], dtype of x: h_t rounded to nearest-even
  *   final_state   [N, D] fp32 (the unrounded h after the last token; initial_state
  *                 for a sequence without tokens), or NULL

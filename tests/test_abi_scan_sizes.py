@@ -1,5 +1,6 @@
-"""Sizes that deltanet_scan_* refuse before a GPU is touched: what the kernels' 32-bit counters of
-tokens and channels do not hold."""
+"""Sizes that deltanet_scan_* and deltanet_step refuse before a GPU is touched: what the kernels'
+32-bit counters of tokens and channels do not hold, tokens without a sequence, slots of more
+requests than the search for repeated ones is made for."""
 import pytest
 
 from deltanet_chunkwise_delta_b200 import _lib as L
@@ -26,3 +27,13 @@ def test_rows_past_the_counters(lib, T, D):
     assert lib.deltanet_scan_fwd(*args(x, g, None, None, out, fin)) == L.DN_ERR_INVALID_ARG
     assert lib.deltanet_scan_bwd(*args(g, out, None, None, x, None, *more, None)) == L.DN_ERR_INVALID_ARG
     assert lib.deltanet_scan_step(*args(x, g, state, None, out)) == L.DN_ERR_INVALID_ARG
+
+
+def test_tokens_of_no_sequence(lib):
+    """cu_seqlens of one entry: nothing would be written, and no kernel run to report it."""
+    x, g, out, dx, dg = (desc([1, 5, 8], L.DN_F32, i) for i in (1, 2, 3, 4, 5))
+    cu = desc([1], L.DN_I32, 6)
+    a = [None if t is None else ref(t) for t in (x, g, None, cu, out, None)] + [None]
+    assert lib.deltanet_scan_fwd(*a) == L.DN_ERR_INVALID_ARG
+    a = [None if t is None else ref(t) for t in (g, out, None, cu, x, None, dx, dg, None)] + [None]
+    assert lib.deltanet_scan_bwd(*a) == L.DN_ERR_INVALID_ARG
