@@ -45,8 +45,12 @@ void launch_step(const StepParams& p, int64_t dk, int64_t dv, int gate, unsigned
     else launch_step<E, 64, 64>(p, gate, grid, s);
 }
 
-// The state cache and slot indices of the step entry points; M rows.
+// The state cache and slot indices of the step entry points; M rows.  Every CTA looks a slot up
+// among those before it (step_slot): with 2^20 requests that is 2^39 reads for every row of CTAs,
+// and with a hundred times as many it would hold the GPU for an hour.
+constexpr int64_t kMaxSlots = int64_t(1) << 20;
 dn_status cache_check(const dn_tensor* state, const dn_tensor* slots, int64_t N) {
+    if (slots && N > kMaxSlots) return DN_ERR_INVALID_ARG;
     if (slots ? !index_ok(slots, 0) || slots->shape[0] != N : state->shape[0] != N) return DN_ERR_INVALID_ARG;
     return state->shape[0] <= kMax31 ? DN_OK : DN_ERR_INVALID_ARG;
 }

@@ -316,7 +316,7 @@ dn_status deltanet_fwd_noalloc(const dn_tensor* q, const dn_tensor* k, const dn_
  *   n_h           writes per token, 1 .. 1024 (with or without g)
  *   state         [M, H, d_k, d_v] fp32, read and written in place; rows that no
  *                 request names stay as they are, and so does a named row where T is 0
- *   slot_idx      int32 [N] device array: the state row of each request; NULL:
+ *   slot_idx      int32 [N] device array, N <= 2^20: the state row of each request; NULL:
  *                 request n uses row n (then M == N).  -1 marks a padding request: no
  *                 state is touched and its rows of out are zero.  Every other index
  *                 must lie in 0 .. M-1 and be named once.  A request whose index is

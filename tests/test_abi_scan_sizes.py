@@ -37,3 +37,14 @@ def test_tokens_of_no_sequence(lib):
     assert lib.deltanet_scan_fwd(*a) == L.DN_ERR_INVALID_ARG
     a = [None if t is None else ref(t) for t in (g, out, None, cu, x, None, dx, dg, None)] + [None]
     assert lib.deltanet_scan_bwd(*a) == L.DN_ERR_INVALID_ARG
+
+
+def test_slots_of_too_many_requests(lib):
+    N = 2 ** 20 + 1
+    at = lambda i, *s, t=L.DN_F32: desc(list(s), t, 1 + i * 2 ** 8)
+    a = [at(0, N, 1, 8), at(1, N, 1, 8), at(2, N, 8), at(3, N, t=L.DN_I32), at(4, N, 1, 8)]
+    assert lib.deltanet_scan_step(*map(ref, a), None) == L.DN_ERR_INVALID_ARG
+    q, k, v, out = (at(i, N, 1, 1, 64, t=L.DN_BF16) for i in range(4))
+    beta, state, slots = at(4, N, 1, 1), at(5, 4, 1, 64, 64), at(6, N, t=L.DN_I32)
+    assert lib.deltanet_step(ref(q), ref(k), ref(v), ref(beta), None, 1, ref(state), ref(slots), ref(out),
+                             None) == L.DN_ERR_INVALID_ARG
