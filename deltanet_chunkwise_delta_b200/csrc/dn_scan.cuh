@@ -359,9 +359,9 @@ struct ScanRuns {
                                           // first half, what comes into the run
     float2 logs[W][32];                   // the logarithms of A0, A1
     uint64_t full[2];                     // the cluster's runs of a tile have arrived
-    // A where it is one factor, in a cluster together with the CTA's other runs; else infinite
+    // A where it is one factor, in a cluster together with the CTA's other runs; else negative
     static __device__ __forceinline__ float factor(float l) {
-        return fabsf(l) > (CL ? 126.f / 8 : 126.f) ? __uint_as_float(0x7f800000u) : scan_pow2(l);
+        return fabsf(l) > (CL ? 126.f / 8 : 126.f) ? -1.f : scan_pow2(l);
     }
     // h and the logarithms of one warp's run; cut: it passes on h alone
     __device__ __forceinline__ void put(int w, float* l, const float* h, bool cut) {
@@ -370,9 +370,6 @@ struct ScanRuns {
         logs[w][lane] = make_float2(l[0], l[1]);
         warp[w][lane] = make_float4(factor(l[0]), factor(l[1]), h[0], h[1]);
     }
-    static __device__ __forceinline__ bool is_far(float4 run) {
-        return run.x == __uint_as_float(0x7f800000u) || run.y == __uint_as_float(0x7f800000u);
-    }
     // a run with factors that run_map<.., true> takes
     __device__ __forceinline__ float4 farther(int w, float4 run) const {
         const float2 l = logs[w][threadIdx.x & 31];
@@ -380,6 +377,10 @@ struct ScanRuns {
     }
 };
 
+// the signs of a run's A among others' (NaN, the mark, has none)
+__device__ __forceinline__ unsigned run_signs(unsigned signs, float4 run) {
+    return signs | __float_as_uint(run.x) | __float_as_uint(run.y);
+}
 template <bool PACKED, bool FAR>
 __device__ __forceinline__ void run_through(float4 r, float& c0, float& c1) {
     c0 = run_map<PACKED, FAR>(r.x, r.z, c0);
@@ -425,9 +426,10 @@ __device__ __forceinline__ int scan_join(ScanRuns<W, CL>& sm, float4* cta, int t
         const int par = i & 1;
         bar_sync(kBarRuns, (W + 1) * 32);
         float4 run[W];
-        bool far = false;
+        unsigned signs = 0;
 #pragma unroll
-        for (int w = 0; w < W; ++w) far |= sm.is_far(run[w] = sm.warp[w][lane]);
+        for (int w = 0; w < W; ++w) signs = run_signs(signs, run[w] = sm.warp[w][lane]);
+        const bool far = (int)signs < 0;
         if constexpr (!CL) {
             auto through = [&](auto any) {
 #pragma unroll
@@ -484,14 +486,14 @@ __device__ __forceinline__ int scan_join(ScanRuns<W, CL>& sm, float4* cta, int t
             } else {
                 float c0 = 0.f, c1 = 0.f;
                 const float before[2] = {carry[0], carry[1]};
-                bool again = false;
+                signs = 0;
                 for (int r = 0; r < K; ++r) {
                     if (r == (int)rank) c0 = carry[0], c1 = carry[1];
                     const float4 run = cta[(par * K + r) * 32 + lane];
-                    again |= run.x < 0.f || run.y < 0.f;
+                    signs = run_signs(signs, run);
                     run_through<PACKED, false>(run, carry[0], carry[1]);
                 }
-                if (again) {
+                if ((int)signs < 0) {
                     carry[0] = before[0], carry[1] = before[1];
                     for (int r = 0; r < K; ++r) {
                         if (r == (int)rank) c0 = carry[0], c1 = carry[1];
