@@ -536,7 +536,7 @@ def deltanet_scan_fwd(x: torch.Tensor, g: torch.Tensor,
     x [B, T, D] bf16 or fp32; g [B, T, D] fp32 (or bf16 with bf16 x), ln of the decay;
     initial_state [N, D] fp32 or None; cu_seqlens int32 [N+1] or None.  Returns (out,
     final_state or None): every h_t in the dtype of x and the last one of each sequence
-    in fp32."""
+    in fp32.  Outside autograd: ``deltanet_scan_bwd`` gives the gradients."""
     if stream is None:
         r = (_call or _short()).scan_fwd(x, g, initial_state, cu_seqlens, out, final_state,
                                          output_final_state)
@@ -625,7 +625,7 @@ def deltanet_norm_fwd(y: torch.Tensor, weight: Optional[torch.Tensor] = None,
     y, gate [.., d] in one dtype (bf16 or fp32); residual in that dtype or fp32; weight,
     scale, next_weight [d] fp32 or bf16; activation "silu" or "sigmoid".  Returns (out,
     residual_out): without residual (y2, None); with it (n, r'), n None without
-    next_weight."""
+    next_weight.  Outside autograd: ``deltanet_norm_bwd`` gives the gradients."""
     act = _activation(activation)
     if stream is None:
         r = (_call or _short()).norm_fwd(y, weight, gate, residual, scale, next_weight, act, eps,

@@ -115,8 +115,8 @@ bool scan_pairs(const ScanParams& p, int32_t x, int32_t g, bool bwd) {
 // CTAs per cluster: enough for most SMs, and on to one and a third of them where a row is
 // split anyway (a cluster's CTAs often sit two to an SM), each with one and a half tiles or
 // more.  Measured with 1, 2, 4, 8 (forward, bf16, fp32 gates): 16 channel tiles of 32768 tokens
-// 415, 201, 105, 87 us; 32 of 16384 208, 104, 57, 52; 64 of 512 9.3, 8.8, 7.9, 11.5; 256 of
-// 2048 51, 56, 67, 94; 128 of 1024 17, 18, 24, 29 us.
+// 334, 180, 95, 69 us; 32 of 16384 172, 93, 52, 50; 64 of 512 8.3, 8.7, 8.0, 10.9; 256 of
+// 2048 44, 51, 59, 85; 128 of 1024 15, 17, 23, 28 us.
 int scan_cluster(int64_t items, int64_t T, int tokens, int sms) {
     int K = 1;
     while (K < kScanMaxCluster && (items * K < sms * 5 / 6 || (K > 1 && items * K < sms * 4 / 3)) &&
@@ -147,8 +147,8 @@ dn_status scan_launch(Kern* kern, int64_t items, int K, int threads, int smem, i
 
 // Up to so many tokens a thread walks its channels, and up to the larger number where that
 // fills the GPU (four CTAs of walkers on an SM).  2048 channels, bf16 with fp32 gates, walkers
-// against tiles: 32 tokens of 512 rows 47 and 151 us, 128 of 128 rows 47 and 65, 192 of 85 rows
-// 50 and 57, 512 of 32 rows 85 and 51; backward 32 of 512 80 and 225, 512 of 128 346 and 301.
+// against tiles: 32 tokens of 512 rows 45 and 158 us, 128 of 128 rows 45 and 62, 192 of 85 rows
+// 48 and 55, 512 of 32 rows 85 and 49; backward 32 of 512 80 and 240, 512 of 128 343 and 302.
 constexpr int kScanSerialT = 16, kScanSerialManyT = 192;
 
 // 16-byte copies: bit 0 for x, 1 for g, 2 for h.
@@ -166,9 +166,9 @@ dn_status scan_tiled(ScanParams& p, int dev, int sms, cudaStream_t stream) {
     const int64_t items = (int64_t)(PACKED ? 1 : p.B) * ((p.D + 63) / 64);
     // Held runs where the instructions bound the tiles, and tokens per run as many as registers
     // or two CTAs' shared memory allow.  Held and read twice: rows of one CTA, 8 x 2048 x 2048,
-    // bf16 gates 38 and 43 us, fp32 gates 53 and 50, all fp32 74 and 70; clusters of 8, 65536 x
-    // 2048 all fp32 270 and 333, 222464 x 2048 all bf16 484 and 586 us; backward 65536 x 2048
-    // 339 and 335, 8 x 2048 x 2048 93 and 90 us.
+    // bf16 gates 35 and 38 us, fp32 gates 45 and 45, all fp32 66 and 64; clusters of 8, 65536 x
+    // 2048 all fp32 278 and 303, 222459 x 2048 packed all bf16 547 and 634 us.  Backward reads
+    // twice (held: 65536 x 2048 339 us, not 335, 8 x 2048 x 2048 93, not 90).
     constexpr bool H1 = !BWD && sizeof(G) == 2, HK = !BWD;
     constexpr int T1 = sizeof(X) == 4 ? 4 : 8, TK = T1 + (HK && EVEN ? 4 : 0);
     constexpr int W1 = kScanWarps<H1>, WK = kScanWarps<HK>;

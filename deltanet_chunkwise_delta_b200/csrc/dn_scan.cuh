@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kScanWalkers) k_scan_bwd_serial(ScanParams p) 
 // have taken its place in shared memory, of a bf16 gate the power is taken twice): fewer
 // instructions and longer runs against one warp more.
 //
-// B200: forward of 8 x 2048 x 2048 (bf16, fp32 gates) 51 us, 80 % of the measured copy rate
-// (256 CTAs: 108 SMs have two of them, 40 have one); of 65536 x 2048 in fp32 270 us, 91 %;
-// backward of 65536 x 2048 (bf16, fp32 gates) 335 us, 85 %.  Packed forward of 222459 x 2048 in
-// bf16 565 us, 74 %; without the 32 sequences' boundaries 484: a tile with one goes the long
+// B200: forward of 8 x 2048 x 2048 (bf16, fp32 gates) 44 us, 93 % of the measured copy rate
+// (256 CTAs: 108 SMs have two of them, 40 have one); of 65536 x 2048 in fp32 280 us, 88 %;
+// backward of 65536 x 2048 (bf16, fp32 gates) 338 us, 85 %.  Packed forward of 222459 x 2048 in
+// bf16 545 us, 76 %; without the 32 sequences' boundaries 500: a tile with one goes the long
 // way in one warp, and the cluster waits for it.
 
 template <bool HELD>
